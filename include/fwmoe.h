@@ -357,6 +357,132 @@ int fw_moe_layer_noalloc(const fw_moe_desc *desc, int32_t T, const void *x,
                          int32_t *sorted_pairs, int32_t *inv_pos, float *out,
                          int32_t *status, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Training products beside the layer (bf16 weights and activations)
+ *
+ * The expert FFN's two products in a form that can be trained and, for a few
+ * rows, served: the gated pair h = f(x Wg^T) * (x Wu^T) (fw_moe_glu_*) and the
+ * linear product y = f(x W^T + b) + residual (fw_moe_linear_*), each with its
+ * backward pass, for one matrix (a dense FFN, the shared expert) or one per
+ * routed expert; and the activation checkpoints in 8 bits that the backward
+ * calls take x from (fw_moe_ckpt_*).
+ *
+ * Rows.  x, h, y, dh, dy, dx, residual are [R][features], contiguous.  With
+ * expert_offsets (int32 [E + 1], as fw_moe_permute writes them) the rows are
+ * expert-major: rows [offsets[e], offsets[e + 1]) belong to expert e; rows
+ * from offsets[E] on are neither read for a result nor written.  NULL (only
+ * with n_experts = 1): all R rows.  Bad offsets are clamped and set
+ * FW_STATUS_BAD_OFFSETS as in fw_moe_forward.  R = 0 is valid: the weight and
+ * bias gradients are then zeros (unchanged with accumulate), as they are for
+ * any expert without rows.
+ *
+ * Numerics.  x, weights, dh and dy are bf16; products are exact in fp32 and
+ * summed in fp32 in a fixed order (results are bitwise reproducible; not the
+ * same bits for every R).  The outputs take one rounding, to out_dtype (h, y;
+ * residual has that type too) or grad_dtype (dx and the weight gradients);
+ * bias and its gradient are fp32.  The backward calls form g, u (z) again from
+ * x; dg, du (dz) are rounded to bf16 in between, so that dx and the weight
+ * gradients behind an activation carry that rounding's (at most 2^-8 relative) per
+ * term whatever grad_dtype is; with FW_FN_NONE the linear product has no such
+ * rounding.  NaN and infinities propagate as in the formulas.
+ *
+ * The call conventions are those above: device pointers, 16-byte aligned
+ * (workspace 256), nothing allocated, asynchronous on `stream`, capturable;
+ * calls that share a workspace must be ordered on one stream (two graphs that
+ * share one must not run at once).  Inputs must not overlap outputs, except
+ * that y may be residual itself. */
+enum { FW_FN_NONE = 0, FW_FN_SILU = 1, FW_FN_GELU_TANH = 2, FW_FN_RELU = 3 };
+
+typedef struct {
+    int32_t in_features;   /* K: multiple of 8, 8..65536 (of 32 with a checkpoint)     */
+    int32_t out_features;  /* N: multiple of 8, 8..65536                               */
+    int32_t n_experts;     /* E: 1..512                                                */
+    int32_t fn;            /* FW_FN_*: f.  GELU is the tanh form
+                              0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)));
+                              f'(0) = 0 for RELU                                       */
+    int32_t ckpt;          /* the backward calls' x: FW_ACT_NONE (bf16), or a checkpoint
+                              FW_ACT_MXFP8 | FW_ACT_INT8 (the forward calls take bf16)  */
+    int32_t out_dtype;     /* FW_F32 | FW_BF16: h or y, and residual                   */
+    int32_t grad_dtype;    /* FW_F32 | FW_BF16: dx and the weight gradients            */
+    int32_t accumulate;    /* 1: weight and bias gradients are added to what is there  */
+} fw_moe_dense_desc;
+
+/* Check a descriptor; FW_OK or the reason it is refused (FW_EUNSUPPORTED: a
+ * checkpoint of rows that are not whole 32-element blocks; FW_EINVAL also for
+ * sizes whose launch HIP could not hold). */
+int fw_moe_dense_validate(const fw_moe_dense_desc *desc);
+
+/* Bytes of workspace the product calls need for up to max_R rows; 0 if the
+ * descriptor is invalid or max_R outside 0..2^20.  Its first 256 bytes hold
+ * the status word (fw_moe_clear_status, fw_moe_read_status). */
+size_t fw_moe_dense_workspace_size(const fw_moe_dense_desc *desc, int32_t max_R);
+
+/* h[r] = f(x[r] Wg[e]^T) * (x[r] Wu[e]^T).
+ * x [R][K] bf16; w_gate, w_up [E][N][K] bf16; h [R][N] out_dtype. */
+int fw_moe_glu_forward(const fw_moe_dense_desc *desc, int32_t R, const void *x,
+                       const void *w_gate, const void *w_up, const int32_t *expert_offsets,
+                       void *h, void *workspace, size_t ws_bytes, void *stream);
+
+/* With g = x Wg^T, u = x Wu^T formed again: dg = dh u f'(g), du = dh f(g),
+ *   dx = dg Wg + du Wu,  dw_gate = dg^T x,  dw_up = du^T x,  h = f(g) u.
+ * x        [R][K] bf16, or the checkpoint's codes (x_scales: its scales; NULL
+ *          with FW_ACT_NONE); gradients are taken at the checkpoint's values
+ * dh       [R][N] bf16
+ * dx       [R][K] grad_dtype or NULL;  dw_gate, dw_up [E][N][K] grad_dtype,
+ *          both or neither NULL;  h [R][N] bf16 or NULL (for the next
+ *          product's weight gradient).  At least one of them. */
+int fw_moe_glu_backward(const fw_moe_dense_desc *desc, int32_t R, const void *x,
+                        const void *x_scales, const void *w_gate, const void *w_up,
+                        const int32_t *expert_offsets, const void *dh, void *dx, void *dw_gate,
+                        void *dw_up, void *h, void *workspace, size_t ws_bytes, void *stream);
+
+/* y[r] = f(x[r] W[e]^T + bias[e]) + residual[r].
+ * x [R][K] bf16; w [E][N][K] bf16; bias [E][N] fp32 or NULL; residual [R][N]
+ * out_dtype or NULL (may be y); y [R][N] out_dtype. */
+int fw_moe_linear_forward(const fw_moe_dense_desc *desc, int32_t R, const void *x, const void *w,
+                          const float *bias, const void *residual,
+                          const int32_t *expert_offsets, void *y, void *workspace,
+                          size_t ws_bytes, void *stream);
+
+/* With z = x W^T + bias formed again (not with FW_FN_NONE): dz = dy f'(z),
+ *   dx = dz W,  dw = dz^T x,  dbias = sum of dz over the expert's rows
+ * (the residual's gradient is dy itself).
+ * x, x_scales as in fw_moe_glu_backward (needed for dw and for z), w (needed
+ * for dx and for z), bias (as in the forward call; unused with FW_FN_NONE);
+ * dy [R][N] bf16; dx [R][K], dw [E][N][K] grad_dtype, dbias [E][N] fp32, each
+ * NULL if not wanted, at least one of them set. */
+int fw_moe_linear_backward(const fw_moe_dense_desc *desc, int32_t R, const void *x,
+                           const void *x_scales, const void *w, const float *bias,
+                           const int32_t *expert_offsets, const void *dy, void *dx, void *dw,
+                           float *dbias, void *workspace, size_t ws_bytes, void *stream);
+
+/* Activation checkpoints: rows kept in 8 bits until the backward pass, in the
+ * blocks of 32 that FW_ACT_MXFP8 and FW_ACT_INT8 use inside the layer (same
+ * codes, same scales).
+ *   FW_ACT_MXFP8: codes E4M3 [R][features], scales E8M0 bytes [R][features/32];
+ *                 1.03 bytes a value, relative step 2^-4, exact in bf16
+ *   FW_ACT_INT8:  codes int8 [R][features], scales fp32 [R][features/32];
+ *                 1.125 bytes a value, step amax / 127 of its block
+ * A block's values read back as bf16(code x scale).  A block that holds a NaN
+ * or an infinity reads back as NaN (scale byte 255, or scale NaN; codes 0) and
+ * sets FW_STATUS_RANGE.  An MXFP8 block's largest values saturate at 448 x
+ * scale (the OCP MX rule), at most 1/8 of the block's maximum. */
+typedef struct {
+    int32_t features;   /* multiple of 32, 32..65536                  */
+    int32_t format;     /* FW_ACT_MXFP8 | FW_ACT_INT8                 */
+    int32_t src_dtype;  /* FW_F32 | FW_BF16: the rows packed          */
+    int32_t dst_dtype;  /* FW_F32 | FW_BF16: the rows read back       */
+} fw_moe_ckpt_desc;
+
+/* x [R][features] src_dtype -> codes, scales.  workspace: at least 256 bytes,
+ * for the status word.  R: 0..2^20. */
+int fw_moe_ckpt_pack(const fw_moe_ckpt_desc *desc, int32_t R, const void *x, void *codes,
+                     void *scales, void *workspace, void *stream);
+
+/* codes, scales -> x [R][features] dst_dtype (the bf16 values in either type). */
+int fw_moe_ckpt_unpack(const fw_moe_ckpt_desc *desc, int32_t R, const void *codes,
+                       const void *scales, void *x, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,8 @@ SCORES = {"softmax": FW_SOFTMAX_RENORM, "sigmoid": FW_SIGMOID_RENORM}
 PATHS = {"auto": FW_PATH_AUTO, "gemv": FW_PATH_GEMV, "gemm": FW_PATH_GEMM}
 FW_ACT_NONE, FW_ACT_MXFP8, FW_ACT_INT8 = 0, 1, 2
 ACT_QUANTS = {"none": FW_ACT_NONE, "mxfp8": FW_ACT_MXFP8, "int8": FW_ACT_INT8}
+FW_FN_NONE, FW_FN_SILU, FW_FN_GELU_TANH, FW_FN_RELU = 0, 1, 2, 3
+FNS = {"none": FW_FN_NONE, "silu": FW_FN_SILU, "gelu_tanh": FW_FN_GELU_TANH, "relu": FW_FN_RELU}
 
 
 class FwMoeError(RuntimeError):
@@ -54,6 +56,34 @@ def make_desc(hidden, n_experts, top_k, ffn, shared_ffn=0, act_dtype="bf16",
                        enum(SCORES, score), enum(PATHS, path), enum(ACT_QUANTS, act_quant))
 
 
+class fw_moe_dense_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "in_features", "out_features", "n_experts", "fn", "ckpt", "out_dtype", "grad_dtype",
+        "accumulate")]
+
+
+class fw_moe_ckpt_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("features", "format", "src_dtype", "dst_dtype")]
+
+
+def make_dense_desc(in_features, out_features, n_experts=1, fn="silu", ckpt="none",
+                    out_dtype="bf16", grad_dtype="bf16", accumulate=False):
+    """A descriptor of the training products (fw_moe_glu_*, fw_moe_linear_*)
+    from readable names or the FW_* integers; ckpt is the form in which the
+    backward calls get x."""
+    enum = lambda table, v: table[v] if isinstance(v, str) else int(v)
+    return fw_moe_dense_desc(in_features, out_features, n_experts, enum(FNS, fn),
+                             enum(ACT_QUANTS, ckpt), enum(DTYPES, out_dtype),
+                             enum(DTYPES, grad_dtype), int(accumulate))
+
+
+def make_ckpt_desc(features, format, src_dtype="bf16", dst_dtype="bf16"):
+    """A descriptor of 8-bit activation checkpoints ("mxfp8" or "int8")."""
+    enum = lambda table, v: table[v] if isinstance(v, str) else int(v)
+    return fw_moe_ckpt_desc(features, enum(ACT_QUANTS, format), enum(DTYPES, src_dtype),
+                            enum(DTYPES, dst_dtype))
+
+
 _lib = None
 
 
@@ -64,6 +94,8 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is not built (run __graft_entry__.build())")
         L = ctypes.CDLL(LIB_PATH)
         P, I, D = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(fw_moe_desc)
+        Z, DD = ctypes.c_size_t, ctypes.POINTER(fw_moe_dense_desc)
+        CD = ctypes.POINTER(fw_moe_ckpt_desc)
         sig = {
             "fw_moe_version": ([], ctypes.c_char_p),
             "fw_moe_validate": ([D], ctypes.c_int),
@@ -80,6 +112,14 @@ def lib():
             "fw_moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "fw_moe_layer_timed": ([D, I] + [P] * 17 + [ctypes.c_size_t, P, P], ctypes.c_int),
             "fw_moe_layer_noalloc": ([D, I] + [P] * 17 + [P], ctypes.c_int),
+            "fw_moe_dense_validate": ([DD], ctypes.c_int),
+            "fw_moe_dense_workspace_size": ([DD, I], Z),
+            "fw_moe_glu_forward": ([DD, I] + [P] * 6 + [Z, P], ctypes.c_int),
+            "fw_moe_glu_backward": ([DD, I] + [P] * 11 + [Z, P], ctypes.c_int),
+            "fw_moe_linear_forward": ([DD, I] + [P] * 7 + [Z, P], ctypes.c_int),
+            "fw_moe_linear_backward": ([DD, I] + [P] * 10 + [Z, P], ctypes.c_int),
+            "fw_moe_ckpt_pack": ([CD, I] + [P] * 5, ctypes.c_int),
+            "fw_moe_ckpt_unpack": ([CD, I] + [P] * 4, ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -218,3 +258,161 @@ def fw_moe_layer_noalloc(desc, T, x, router_w, logit_bias, w_gate, w_up, w_down,
         _ptr(w_up), _ptr(w_down), _ptr(ws_gate), _ptr(ws_up), _ptr(ws_down), _ptr(logits),
         _ptr(topk_ids), _ptr(topk_w), _ptr(expert_offsets), _ptr(sorted_pairs), _ptr(inv_pos),
         _ptr(out), _ptr(status), _stream(stream)))
+
+
+# ---- training products ------------------------------------------------------
+# The kernels read flat row-major memory: a tensor of another size, type or
+# layout, or on another device than the rest, is refused here (ValueError)
+# before the library sees its pointer.  Raw integer pointers pass unchecked.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_OUT = {FW_F32: _F32, FW_BF16: _BF16}
+# element types of a checkpoint's codes and scales
+_CODES = {FW_ACT_MXFP8: ((torch.uint8, torch.float8_e4m3fn), (torch.uint8,)),
+          FW_ACT_INT8: ((torch.int8, torch.uint8), (_F32,))}
+
+
+def _operand(fn, name, t, count, dtypes, device):
+    """Check one tensor argument (None and raw pointers pass); its device."""
+    if t is None or isinstance(t, int):
+        return device
+    if t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
+    if t.numel() != count:
+        raise ValueError(f"{fn}: {name} has {t.numel()} elements, not {count}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not {device}")
+    return t.device
+
+
+def _launch(fn, operands, workspace, ws_bytes, stream, call):
+    """Check the operands (name, tensor, elements, types), then call(workspace
+    bytes, stream) with their device current."""
+    device = None
+    for name, t, count, dtypes in operands:
+        device = _operand(fn, name, t, count, dtypes, device)
+    if ws_bytes is None and workspace is not None:
+        device = _operand(fn, "workspace", workspace, workspace.numel(), (workspace.dtype,),
+                          device)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    if device is not None and device.type != "cuda":
+        raise ValueError(f"{fn}: tensors are on {device}, not on a GPU")
+    if device is None or device.index == torch.cuda.current_device():
+        return _check(fn, call(ws_bytes or 0, _stream(stream)))
+    with torch.cuda.device(device):
+        return _check(fn, call(ws_bytes or 0, _stream(stream)))
+
+
+def _sizes(desc, R):
+    K, N, E = desc.in_features, desc.out_features, desc.n_experts
+    return R * K, R * N, E * N * K, E * N
+
+
+def _x_operands(desc, R, x, x_scales):
+    """The backward calls' x: bf16 rows or a checkpoint."""
+    if desc.ckpt not in _CODES:
+        return [("x", x, R * desc.in_features, (_BF16,))]
+    codes, scales = _CODES[desc.ckpt]
+    return [("x", x, R * desc.in_features, codes),
+            ("x_scales", x_scales, R * (desc.in_features // 32), scales)]
+
+
+def _offsets_operand(desc, offsets):
+    return ("expert_offsets", offsets, desc.n_experts + 1, (_I32,))
+
+
+def fw_moe_dense_validate(desc):
+    return lib().fw_moe_dense_validate(ctypes.byref(desc))
+
+
+def fw_moe_dense_workspace_size(desc, max_R):
+    return lib().fw_moe_dense_workspace_size(ctypes.byref(desc), max_R)
+
+
+def fw_moe_glu_forward(desc, R, x, w_gate, w_up, expert_offsets, h, workspace, ws_bytes=None,
+                       stream=None):
+    xs, ys, ws, _ = _sizes(desc, R)
+    return _launch(
+        "fw_moe_glu_forward",
+        [("x", x, xs, (_BF16,)), ("w_gate", w_gate, ws, (_BF16,)), ("w_up", w_up, ws, (_BF16,)),
+         _offsets_operand(desc, expert_offsets), ("h", h, ys, (_OUT.get(desc.out_dtype),))],
+        workspace, ws_bytes, stream, lambda nb, s: lib().fw_moe_glu_forward(
+            ctypes.byref(desc), R, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(expert_offsets),
+            _ptr(h), _ptr(workspace), nb, s))
+
+
+def fw_moe_glu_backward(desc, R, x, x_scales, w_gate, w_up, expert_offsets, dh, dx, dw_gate,
+                        dw_up, h, workspace, ws_bytes=None, stream=None):
+    xs, ys, ws, _ = _sizes(desc, R)
+    grad = (_OUT.get(desc.grad_dtype),)
+    return _launch(
+        "fw_moe_glu_backward",
+        _x_operands(desc, R, x, x_scales) +
+        [("w_gate", w_gate, ws, (_BF16,)), ("w_up", w_up, ws, (_BF16,)),
+         _offsets_operand(desc, expert_offsets), ("dh", dh, ys, (_BF16,)), ("dx", dx, xs, grad),
+         ("dw_gate", dw_gate, ws, grad), ("dw_up", dw_up, ws, grad), ("h", h, ys, (_BF16,))],
+        workspace, ws_bytes, stream, lambda nb, s: lib().fw_moe_glu_backward(
+            ctypes.byref(desc), R, _ptr(x), _ptr(x_scales), _ptr(w_gate), _ptr(w_up),
+            _ptr(expert_offsets), _ptr(dh), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), _ptr(h),
+            _ptr(workspace), nb, s))
+
+
+def fw_moe_linear_forward(desc, R, x, w, bias, residual, expert_offsets, y, workspace,
+                          ws_bytes=None, stream=None):
+    xs, ys, ws, bs = _sizes(desc, R)
+    out = (_OUT.get(desc.out_dtype),)
+    return _launch(
+        "fw_moe_linear_forward",
+        [("x", x, xs, (_BF16,)), ("w", w, ws, (_BF16,)), ("bias", bias, bs, (_F32,)),
+         ("residual", residual, ys, out), _offsets_operand(desc, expert_offsets),
+         ("y", y, ys, out)],
+        workspace, ws_bytes, stream, lambda nb, s: lib().fw_moe_linear_forward(
+            ctypes.byref(desc), R, _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
+            _ptr(expert_offsets), _ptr(y), _ptr(workspace), nb, s))
+
+
+def fw_moe_linear_backward(desc, R, x, x_scales, w, bias, expert_offsets, dy, dx, dw, dbias,
+                           workspace, ws_bytes=None, stream=None):
+    xs, ys, ws, bs = _sizes(desc, R)
+    grad = (_OUT.get(desc.grad_dtype),)
+    return _launch(
+        "fw_moe_linear_backward",
+        _x_operands(desc, R, x, x_scales) +
+        [("w", w, ws, (_BF16,)), ("bias", bias, bs, (_F32,)),
+         _offsets_operand(desc, expert_offsets), ("dy", dy, ys, (_BF16,)), ("dx", dx, xs, grad),
+         ("dw", dw, ws, grad), ("dbias", dbias, bs, (_F32,))],
+        workspace, ws_bytes, stream, lambda nb, s: lib().fw_moe_linear_backward(
+            ctypes.byref(desc), R, _ptr(x), _ptr(x_scales), _ptr(w), _ptr(bias),
+            _ptr(expert_offsets), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(workspace), nb,
+            s))
+
+
+def _ckpt_operands(desc, R, codes, scales):
+    code_types, scale_types = _CODES.get(desc.format, ((), ()))
+    return [("codes", codes, R * desc.features, code_types),
+            ("scales", scales, R * (desc.features // 32), scale_types)]
+
+
+def fw_moe_ckpt_pack(desc, R, x, codes, scales, workspace, stream=None):
+    """workspace: a uint8 tensor of at least 256 bytes (its status word)."""
+    if workspace is not None and not isinstance(workspace, int) and \
+            workspace.numel() * workspace.element_size() < 256:
+        raise FwMoeError("fw_moe_ckpt_pack", FW_EWORKSPACE)
+    return _launch(
+        "fw_moe_ckpt_pack",
+        [("x", x, R * desc.features, (_OUT.get(desc.src_dtype),))] +
+        _ckpt_operands(desc, R, codes, scales),
+        workspace, None if not isinstance(workspace, int) else 256, stream,
+        lambda nb, s: lib().fw_moe_ckpt_pack(ctypes.byref(desc), R, _ptr(x), _ptr(codes),
+                                             _ptr(scales), _ptr(workspace), s))
+
+
+def fw_moe_ckpt_unpack(desc, R, codes, scales, x, stream=None):
+    return _launch(
+        "fw_moe_ckpt_unpack",
+        _ckpt_operands(desc, R, codes, scales) +
+        [("x", x, R * desc.features, (_OUT.get(desc.dst_dtype),))],
+        None, 0, stream,
+        lambda nb, s: lib().fw_moe_ckpt_unpack(ctypes.byref(desc), R, _ptr(codes), _ptr(scales),
+                                               _ptr(x), s))

@@ -1,0 +1,181 @@
+"""The training products' and checkpoints' ABI without a GPU: what is refused,
+and with which code, before anything is enqueued; and the binding's checks."""
+
+import ctypes
+
+import pytest
+import torch
+
+from sparse_moe_block_amd import fwmoe as fw
+
+BF16 = torch.bfloat16
+
+
+def desc(**kw):
+    d = dict(in_features=256, out_features=136, n_experts=1, fn="silu")
+    d.update(kw)
+    return fw.make_dense_desc(**d)
+
+
+@pytest.mark.parametrize("field,value,code", [
+    ("in_features", 0, fw.FW_EINVAL), ("in_features", 12, fw.FW_EINVAL),
+    ("in_features", 65544, fw.FW_EINVAL), ("out_features", -8, fw.FW_EINVAL),
+    ("out_features", 4, fw.FW_EINVAL), ("n_experts", 0, fw.FW_EINVAL),
+    ("n_experts", 513, fw.FW_EINVAL), ("fn", 4, fw.FW_EINVAL), ("fn", -1, fw.FW_EINVAL),
+    ("ckpt", 3, fw.FW_EINVAL), ("ckpt", -1, fw.FW_EINVAL), ("out_dtype", 2, fw.FW_EINVAL),
+    ("grad_dtype", -1, fw.FW_EINVAL), ("accumulate", 2, fw.FW_EINVAL)])
+def test_descriptors(field, value, code):
+    d = desc()
+    assert fw.fw_moe_dense_validate(d) == fw.FW_OK
+    setattr(d, field, value)
+    assert fw.fw_moe_dense_validate(d) == code
+    assert fw.fw_moe_dense_workspace_size(d, 16) == 0
+
+
+def test_checkpoints_need_whole_blocks():
+    for ckpt in ("mxfp8", "int8"):
+        assert fw.fw_moe_dense_validate(desc(ckpt=ckpt)) == fw.FW_OK
+        assert fw.fw_moe_dense_validate(desc(ckpt=ckpt, in_features=264)) == fw.FW_EUNSUPPORTED
+    assert fw.fw_moe_dense_validate(desc(in_features=264)) == fw.FW_OK
+
+
+def test_sizes_beyond_a_launch():
+    assert fw.fw_moe_dense_validate(desc(n_experts=512, in_features=65536,
+                                         out_features=65536)) == fw.FW_EINVAL
+    assert fw.fw_moe_dense_validate(desc(in_features=65536, out_features=65536)) == fw.FW_OK
+    d = desc(in_features=65536, out_features=65536)
+    assert fw.fw_moe_dense_workspace_size(d, 1 << 20) == 0
+    assert fw.fw_moe_dense_workspace_size(d, 1 << 14) > 0
+    d = desc()
+    assert fw.fw_moe_dense_workspace_size(d, 1 << 20) > 0
+    assert fw.fw_moe_dense_workspace_size(d, (1 << 20) + 1) == 0
+    assert fw.fw_moe_dense_workspace_size(d, -1) == 0
+
+
+def test_workspace_grows_with_rows():
+    d = desc(n_experts=8)
+    sizes = [fw.fw_moe_dense_workspace_size(d, R) for R in (0, 1, 100, 5000)]
+    assert 256 < sizes[0] < sizes[1] < sizes[2] < sizes[3]
+    # a checkpoint's values are laid out in the workspace too
+    assert fw.fw_moe_dense_workspace_size(desc(ckpt="int8"), 5000) > \
+        fw.fw_moe_dense_workspace_size(desc(), 5000)
+
+
+# One call of each product with placeholder addresses; a refusal must come
+# before any of them is used.
+CALLS = {
+    "fw_moe_glu_forward": ["x", "wg", "wu", "off", "out"],
+    "fw_moe_glu_backward": ["x", "xs", "wg", "wu", "off", "dy", "dx", "dwg", "dwu", "h"],
+    "fw_moe_linear_forward": ["x", "w", "bias", "res", "off", "out"],
+    "fw_moe_linear_backward": ["x", "xs", "w", "bias", "off", "dy", "dx", "dw", "db"],
+}
+
+
+def call(name, d, R=8, ws=256, nbytes=None, **over):
+    args = {a: 16 for a in CALLS[name]}
+    if "off" not in over and d.n_experts == 1:
+        args["off"] = None
+    if d.ckpt == fw.FW_ACT_NONE and "xs" in args:
+        args["xs"] = None
+    args.update(over)
+    if nbytes is None:
+        nbytes = fw.fw_moe_dense_workspace_size(d, max(0, min(R, 1 << 20)))
+    return getattr(fw.lib(), name)(ctypes.byref(d), R, *[args[a] for a in CALLS[name]], ws,
+                                   nbytes, None)
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_shared_refusals(name):
+    d = desc()
+    need = fw.fw_moe_dense_workspace_size(d, 8)
+    assert call(name, d, R=-1) == fw.FW_EINVAL
+    assert call(name, d, R=(1 << 20) + 1) == fw.FW_EINVAL
+    assert call(name, d, ws=None) == fw.FW_EINVAL
+    assert call(name, d, ws=128) == fw.FW_EALIGN
+    assert call(name, d, nbytes=need - 1) == fw.FW_EWORKSPACE
+    assert call(name, desc(in_features=12)) == fw.FW_EINVAL
+    assert call(name, desc(n_experts=4), off=None) == fw.FW_EINVAL
+    assert call(name, desc(n_experts=4), off=24) == fw.FW_EALIGN
+    for a in CALLS[name]:
+        if a not in ("off",) and not (a == "xs"):
+            assert call(name, d, **{a: 24}) == fw.FW_EALIGN, a
+    assert getattr(fw.lib(), name)(None, 8, *[16] * len(CALLS[name]), 256, need, None) == \
+        fw.FW_EINVAL
+
+
+def test_missing_operands():
+    d = desc()
+    for a in ("x", "wg", "wu", "out"):
+        assert call("fw_moe_glu_forward", d, **{a: None}) == fw.FW_EINVAL
+    for a in ("x", "w", "out"):
+        assert call("fw_moe_linear_forward", d, **{a: None}) == fw.FW_EINVAL
+    for a in ("x", "wg", "wu", "dy", "dwg", "dwu"):   # one weight gradient without the other
+        assert call("fw_moe_glu_backward", d, **{a: None}) == fw.FW_EINVAL
+    nothing = dict(dx=None, dwg=None, dwu=None, h=None)
+    assert call("fw_moe_glu_backward", d, **nothing) == fw.FW_EINVAL
+    for a in ("x", "w", "dy"):
+        assert call("fw_moe_linear_backward", d, **{a: None}) == fw.FW_EINVAL
+    assert call("fw_moe_linear_backward", d, dx=None, dw=None, db=None) == fw.FW_EINVAL
+    none = desc(fn="none")   # without an activation x serves dw alone and w dx alone
+    assert call("fw_moe_linear_backward", none, x=None) == fw.FW_EINVAL
+    assert call("fw_moe_linear_backward", none, w=None) == fw.FW_EINVAL
+    q = desc(ckpt="int8")
+    for name in ("fw_moe_glu_backward", "fw_moe_linear_backward"):
+        assert call(name, q, xs=None) == fw.FW_EINVAL
+        assert call(name, q, xs=24) == fw.FW_EALIGN
+
+
+def test_forward_without_rows_is_nothing_to_do():
+    d = desc()
+    for name in ("fw_moe_glu_forward", "fw_moe_linear_forward"):
+        assert call(name, d, R=0, ws=None, x=None, out=None) == fw.FW_OK
+
+
+def test_ckpt_refusals():
+    def pack(d, R=4, x=16, codes=16, scales=16, ws=256):
+        return fw.lib().fw_moe_ckpt_pack(ctypes.byref(d), R, x, codes, scales, ws, None)
+
+    def unpack(d, R=4, codes=16, scales=16, x=16):
+        return fw.lib().fw_moe_ckpt_unpack(ctypes.byref(d), R, codes, scales, x, None)
+    for kw in (dict(features=0), dict(features=48), dict(features=65568), dict(format="none"),
+               dict(format=3), dict(src_dtype=5), dict(dst_dtype=-1)):
+        d = fw.make_ckpt_desc(**{**dict(features=64, format="int8"), **kw})
+        assert pack(d) == fw.FW_EINVAL and unpack(d) == fw.FW_EINVAL
+    d = fw.make_ckpt_desc(64, "mxfp8")
+    assert pack(d, R=0, x=None) == fw.FW_OK and unpack(d, R=0, x=None) == fw.FW_OK
+    assert pack(d, R=-1) == fw.FW_EINVAL and unpack(d, R=(1 << 20) + 1) == fw.FW_EINVAL
+    big = fw.make_ckpt_desc(65536, "mxfp8")
+    assert pack(big, R=1 << 20) == fw.FW_EINVAL and unpack(big, R=1 << 20) == fw.FW_EINVAL
+    for a in ("x", "codes", "scales"):
+        assert pack(d, **{a: None}) == fw.FW_EINVAL and unpack(d, **{a: None}) == fw.FW_EINVAL
+        assert pack(d, **{a: 24}) == fw.FW_EALIGN and unpack(d, **{a: 24}) == fw.FW_EALIGN
+    assert pack(d, ws=None) == fw.FW_EINVAL and pack(d, ws=128) == fw.FW_EALIGN
+
+
+def test_binding_refuses_tensors_the_kernels_cannot_read():
+    """Another type, size, layout or device never reaches the library."""
+    d = desc(in_features=64, out_features=64)
+    x, w = torch.zeros(4, 64, dtype=BF16), torch.zeros(64, 64, dtype=BF16)
+    ws = torch.zeros(fw.fw_moe_dense_workspace_size(d, 4), dtype=torch.uint8)
+    good = dict(x=x, w_gate=w, w_up=w, expert_offsets=None, h=torch.zeros(4, 64, dtype=BF16),
+                workspace=ws)
+    wide = torch.zeros(4, 128, dtype=BF16)
+    for kw, text in ((dict(x=x.float()), "x is torch.float32"),
+                     (dict(x=wide), "x has 512 elements, not 256"),
+                     (dict(x=wide[:, ::2]), "x is not contiguous"),
+                     (dict(w_gate=w.t()), "w_gate is not contiguous"),
+                     (dict(h=torch.zeros(4, 64)), "h is torch.float32"),
+                     (dict(expert_offsets=torch.zeros(2, dtype=torch.int64)),
+                      "expert_offsets is torch.int64"),
+                     (dict(expert_offsets=torch.zeros(3, dtype=torch.int32)),
+                      "expert_offsets has 3 elements"),
+                     (dict(h=torch.zeros(4, 64, dtype=BF16, device="meta")), "h is on meta"),
+                     (dict(), "not on a GPU")):
+        with pytest.raises(ValueError, match=text):
+            fw.fw_moe_glu_forward(d, 4, **{**good, **kw})
+    c = fw.make_ckpt_desc(64, "int8", src_dtype="f32")
+    with pytest.raises(ValueError, match="x is torch.bfloat16"):
+        fw.fw_moe_ckpt_pack(c, 4, x, torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 2), ws)
+    with pytest.raises(fw.FwMoeError, match="workspace"):
+        fw.fw_moe_ckpt_pack(c, 4, x.float(), torch.zeros(4, 64, dtype=torch.int8),
+                            torch.zeros(4, 2), ws[:128])
