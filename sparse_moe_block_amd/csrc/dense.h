@@ -47,6 +47,7 @@ struct RowsArgs {
     const int4 *tiles;         // row tiles, or nullptr: all R rows of expert 0
     WsHeader *hdr;
     int max_tiles;
+    int tile_rows;             // 128 or 256 (dense_tile_rows)
     const float *bias;         // [E][Np] or nullptr
     const void *residual;      // out's type, or nullptr
     const uint16_t *dy;        // bf16 [R][Np]: the arriving gradient
@@ -55,6 +56,10 @@ struct RowsArgs {
     uint16_t *dz;              // kGluGrad: dg, then du at + R * Np; kLinGrad: dz
     float *bpart;              // kLinGrad: [row tile][Np] or nullptr
 };
+constexpr int kCus = 256;      // the MI355X's compute units
+// Rows of a row tile: one choice per call when the tiles come from a schedule,
+// per product (`cols` output columns) otherwise.
+int dense_tile_rows(int R, int E, int cols, bool grouped);
 hipError_t launch_rows(DenseOp op, const RowsArgs &a, hipStream_t s);
 
 // Weight gradients: dw[e][n][k] = sum over the rows r of e of dz[r][n] x[r][k].
@@ -74,12 +79,13 @@ int64_t rows_tiles(int R, int E, int Np);
 // db[e][n] = sum over e's rows of dz: per row tile (colsum: from bf16 rows
 // dy; kLinGrad writes the same partials itself), then over e's tiles in order.
 hipError_t launch_colsum(const uint16_t *dy, int R, int N, const int4 *tiles, WsHeader *hdr,
-                         int max_tiles, float *bpart, hipStream_t s);
+                         int max_tiles, int tile_rows, float *bpart, hipStream_t s);
 hipError_t launch_bias_grad(const float *bpart, const int32_t *offsets, int R, int E, int N,
-                            float *db, int accumulate, hipStream_t s);
+                            int max_tiles, int tile_rows, float *db, int accumulate,
+                            hipStream_t s);
 
-hipError_t launch_dense_schedule(const int32_t *offsets, int E, int R, const DenseWs &L, char *ws,
-                                 hipStream_t s);
+hipError_t launch_dense_schedule(const int32_t *offsets, int E, int R, int tile_rows,
+                                 const DenseWs &L, char *ws, hipStream_t s);
 
 // 8-bit blocks (ckpt.hip)
 hipError_t launch_ckpt_pack(int format, int64_t blocks, const void *src, int src_bf16,

@@ -11,26 +11,42 @@
 // bf16 products that follow; the bias gradient is summed before that rounding.
 #include <math.h>
 
+#include <type_traits>
+
 #include "dense_core.h"
 #include "stages.h"
 
 namespace fw {
 namespace {
 
-// Four consecutive output values at p (bf16 or fp32).
-__device__ __forceinline__ void store4(void *out, int f32, size_t at, const float *v) {
-    if (f32)
-        *(float4 *)((float *)out + at) = float4{v[0], v[1], v[2], v[3]};
-    else
-        *(uint2 *)((uint16_t *)out + at) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-}
-__device__ __forceinline__ void load4(const void *in, int f32, size_t at, float *v) {
+// Eight consecutive values in memory, bf16 or fp32.
+struct Eight {
+    uint4 r[2];   // bf16: r[0]
+};
+__device__ __forceinline__ void load8(Eight &e, const void *in, int f32, size_t at) {
     if (f32) {
-        const float4 f = *(const float4 *)((const float *)in + at);
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        const uint4 *p = (const uint4 *)((const float *)in + at);
+        e.r[0] = p[0];
+        e.r[1] = p[1];
     } else {
-        const uint2 u = *(const uint2 *)((const uint16_t *)in + at);
-        v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+        e.r[0] = *(const uint4 *)((const uint16_t *)in + at);
+    }
+}
+__device__ __forceinline__ void values8(const Eight &e, int f32, float *v) {
+    const uint32_t w[8] = {e.r[0].x, e.r[0].y, e.r[0].z, e.r[0].w,
+                           e.r[1].x, e.r[1].y, e.r[1].z, e.r[1].w};
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+        v[t] = f32 ? __uint_as_float(w[t]) : (t & 1) ? bf16_hi(w[t / 2]) : bf16_lo(w[t / 2]);
+}
+__device__ __forceinline__ void store8(void *out, int f32, size_t at, const float *v) {
+    if (f32) {
+        float4 *p = (float4 *)((float *)out + at);
+        p[0] = float4{v[0], v[1], v[2], v[3]};
+        p[1] = float4{v[4], v[5], v[6], v[7]};
+    } else {
+        *(uint4 *)((uint16_t *)out + at) = uint4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                 pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
     }
 }
 
@@ -57,14 +73,21 @@ __device__ __forceinline__ int dense_tile(int row_tiles, int col_tiles, int &ct)
     return r0 + in % n;
 }
 
-template <DenseOp OP> struct RowShape {
-    using T = Shape<128, 128, 2, 2, OP == kInput, false, OP == kGlu || OP == kGluGrad>;
+// Tile shapes.  Large: 256 x 256, eight wavefronts of 64 x 128 outputs, one
+// workgroup a CU.  Small: 128 x 128, four wavefronts of 64 x 64, two workgroups
+// a CU.
+template <DenseOp OP, bool LARGE> struct RowShape {
+    static constexpr bool kAcross = OP == kInput, kDual = OP == kGlu || OP == kGluGrad;
+    using T = std::conditional_t<LARGE, Shape<256, 256, 4, 2, kAcross, false, kDual>,
+                                 Shape<128, 128, 2, 2, kAcross, false, kDual>>;
 };
 
 // One (row tile, column tile).
-template <DenseOp OP>
-__global__ __launch_bounds__(256, 2) void rows_kernel(RowsArgs a, int col_tiles, int row_tiles) {
-    using S = typename RowShape<OP>::T;
+template <DenseOp OP, bool LARGE>
+__global__ __launch_bounds__(LARGE ? 512 : 256, LARGE ? 1 : 2) void rows_kernel(RowsArgs a,
+                                                                               int col_tiles,
+                                                                               int row_tiles) {
+    using S = typename RowShape<OP, LARGE>::T;
     __shared__ uint4 P0[S::PChunks];
     __shared__ uint4 P1[S::PChunks];
     __shared__ uint4 Q0[S::QChunks];
@@ -99,102 +122,92 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(RowsArgs a, int col_tiles,
     auto pb = [&](int) {
         return Operand{(const char *)(a.w1 + we + (size_t)c0 * a.Kd), cols, qpitch, 0};
     };
-    f16v acc[S::PI][S::QJ];
+    f4 acc[S::PI][S::QJ];
     tile_product<S>(acc, P0, P1, Q0, Q1, wave, lane, a.Kd, a.nseg, p, pb, q);
 
-    // acc[i][j][4 m + t]: row qrow(wq, j) + lane % 32, column prow(wp, i) +
-    // 8 m + 4 (lane / 32) + t
-    const int wp = wave % S::WP, wq = wave / S::WP, g4 = 4 * (lane >> 5);
     const size_t dzu = (size_t)a.R * a.Np;   // du behind dg
-    if constexpr (OP == kLinGrad) {
-        // per-column sums over the tile's rows, through LDS
-        __syncthreads();
+    float bias[8], colsum[8];
+    {
+        // the columns a lane is handed are the same for every row
+        const int col = c0 + wave % S::WP * kOutCols<S> + lane % (kOutCols<S> / 8) * 8;
+        Eight e{};
+        if ((OP == kLinear || OP == kLinGrad) && a.bias && col < c0 + cols)
+            load8(e, a.bias, 1, (size_t)expert * a.Np + col);
+        values8(e, 1, bias);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) colsum[t] = 0.f;
     }
-    float colsum[S::PI][16];
-    if constexpr (OP == kLinGrad) {
+    auto inside = [&](int row, int col) { return row < rows && col < cols; };
+    auto place = [&](int row, int col) { return (size_t)(rb + row) * a.Np + c0 + col; };
+    auto fetch = [&](int row, int col) {
+        Eight e{};
+        if constexpr (OP == kGluGrad || OP == kLinGrad) {
+            if (inside(row, col)) load8(e, a.dy, 0, place(row, col));
+        } else if constexpr (OP == kLinear) {
+            if (a.residual && inside(row, col)) load8(e, a.residual, a.out_f32, place(row, col));
+        }
+        return e;
+    };
+    hand_out<S>(acc, P0, wave, lane, fetch,
+                [&](int row, int col, float *v, const float *u, const Eight &e) {
+        if (!inside(row, col)) return;
+        const size_t at = place(row, col);
+        if constexpr (OP == kGlu) {
 #pragma unroll
-        for (int i = 0; i < S::PI; ++i)
+            for (int t = 0; t < 8; ++t) v[t] = act_value(a.fn, v[t]) * u[t];
+            store8(a.out, a.out_f32, at, v);
+        } else if constexpr (OP == kGluGrad) {
+            float dh[8], dg[8], du[8];
+            values8(e, 0, dh);
 #pragma unroll
-            for (int v = 0; v < 16; ++v) colsum[i][v] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < S::QJ; ++j) {
-        const int row = S::qrow(wq, j) + (lane & 31);
-        const size_t at0 = (size_t)(rb + row) * a.Np;
-#pragma unroll
-        for (int i = 0; i < (S::DUAL ? 1 : S::PI); ++i)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int col = c0 + S::prow(wp, i) + 8 * m + g4;
-                if (row >= rows || col >= a.Np || col >= c0 + cols) continue;
-                const size_t at = at0 + col;
-                float v[4];
-                if constexpr (OP == kGlu) {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        v[t] = act_value(a.fn, acc[0][j][4 * m + t]) * acc[1][j][4 * m + t];
-                    store4(a.out, a.out_f32, at, v);
-                } else if constexpr (OP == kGluGrad) {
-                    float dh[4], dg[4], du[4];
-                    load4(a.dy, 0, at, dh);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        float f, df;
-                        const float u = acc[1][j][4 * m + t];
-                        act_both(a.fn, acc[0][j][4 * m + t], f, df);
-                        v[t] = f * u;
-                        dg[t] = dh[t] * u * df;
-                        du[t] = dh[t] * f;
-                    }
-                    store4(a.dz, 0, at, dg);
-                    store4(a.dz, 0, dzu + at, du);
-                    if (a.out) store4(a.out, 0, at, v);
-                } else if constexpr (OP == kLinear || OP == kLinGrad) {
-                    float b[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (a.bias) load4(a.bias, 1, (size_t)expert * a.Np + col, b);
-                    if constexpr (OP == kLinear) {
-                        float r[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (a.residual) load4(a.residual, a.out_f32, at, r);
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            v[t] = act_value(a.fn, acc[i][j][4 * m + t] + b[t]);
-                            if (a.residual) v[t] += r[t];
-                        }
-                        store4(a.out, a.out_f32, at, v);
-                    } else {
-                        float dy[4];
-                        load4(a.dy, 0, at, dy);
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            float f, df;
-                            act_both(a.fn, acc[i][j][4 * m + t] + b[t], f, df);
-                            v[t] = dy[t] * df;
-                            colsum[i][4 * m + t] += v[t];
-                        }
-                        store4(a.dz, 0, at, v);
-                    }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) v[t] = acc[i][j][4 * m + t];
-                    store4(a.out, a.out_f32, at, v);
-                }
+            for (int t = 0; t < 8; ++t) {
+                float f, df;
+                act_both(a.fn, v[t], f, df);
+                v[t] = f * u[t];
+                dg[t] = dh[t] * u[t] * df;
+                du[t] = dh[t] * f;
             }
-    }
+            store8(a.dz, 0, at, dg);
+            store8(a.dz, 0, dzu + at, du);
+            if (a.out) store8(a.out, 0, at, v);
+        } else if constexpr (OP == kLinear) {
+            float r[8];
+            values8(e, a.out_f32, r);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                v[t] = act_value(a.fn, v[t] + bias[t]);
+                if (a.residual) v[t] += r[t];
+            }
+            store8(a.out, a.out_f32, at, v);
+        } else if constexpr (OP == kLinGrad) {
+            float dy[8];
+            values8(e, 0, dy);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                float f, df;
+                act_both(a.fn, v[t] + bias[t], f, df);
+                v[t] = dy[t] * df;
+                colsum[t] += v[t];
+            }
+            store8(a.dz, 0, at, v);
+        } else {
+            store8(a.out, a.out_f32, at, v);
+        }
+    });
     if constexpr (OP == kLinGrad) {
         if (!a.bpart) return;
-        // over the 32 rows a lane group holds, then over the wavefronts of the
-        // column, in a fixed order
-        float *part = (float *)P0;   // [WQ][BP]
+        // over the lanes that hold the same columns, then over the wavefronts
+        // of the column, in a fixed order
+        constexpr int CW = kOutCols<S>, LR = CW / 8;
+        const int wp = wave % S::WP, wq = wave / S::WP;
+        float *part = (float *)Q0;   // [WQ][BP]
 #pragma unroll
-        for (int i = 0; i < S::PI; ++i)
+        for (int t = 0; t < 8; ++t) {
+            float s = colsum[t];
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                float s = colsum[i][v];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor(s, o);
-                if ((lane & 31) == 0)
-                    part[wq * S::BP + S::prow(wp, i) + 8 * (v >> 2) + g4 + (v & 3)] = s;
-            }
+            for (int o = 32; o >= LR; o >>= 1) s += __shfl_xor(s, o);
+            if (lane < LR) part[wq * S::BP + wp * CW + 8 * lane + t] = s;
+        }
         __syncthreads();
         for (int c = threadIdx.x; c < cols; c += S::Threads) {
             float s = 0.f;
@@ -206,10 +219,14 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(RowsArgs a, int col_tiles,
 }
 
 // dw tiles: Q = output features (rows of dw), P = input features.
-using GradShape = Shape<128, 128, 2, 2, true, true, false>;
+template <bool LARGE>
+using GradShape = std::conditional_t<LARGE, Shape<256, 256, 4, 2, true, true, false>,
+                                     Shape<128, 128, 2, 2, true, true, false>>;
 
-__global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs a, int nt, int kt, int tiles) {
-    using S = GradShape;
+template <bool LARGE>
+__global__ __launch_bounds__(LARGE ? 512 : 256, LARGE ? 1 : 2) void grad_kernel(GradArgs a, int nt,
+                                                                               int kt, int tiles) {
+    using S = GradShape<LARGE>;
     __shared__ uint4 P0[S::PChunks];
     __shared__ uint4 P1[S::PChunks];
     __shared__ uint4 Q0[S::QChunks];
@@ -235,42 +252,38 @@ __global__ __launch_bounds__(256, 2) void grad_kernel(GradArgs a, int nt, int kt
     auto p = [&](int) {
         return Operand{(const char *)x, 0, 2u * (uint32_t)a.K, 2u * (uint32_t)k0};
     };
-    f16v acc[S::PI][S::QJ];
+    f4 acc[S::PI][S::QJ];
     tile_product<S>(acc, P0, P1, Q0, Q1, wave, lane, e - b, 1, p, p, q);
 
-    const int wp = wave % S::WP, wq = wave / S::WP, g4 = 4 * (lane >> 5);
     void *dw = mat ? a.dw1 : a.dw0;
+    auto inside = [&](int n, int k) { return n0 + n < a.N && k0 + k < a.K; };
+    auto place = [&](int n, int k) { return ((size_t)expert * a.N + n0 + n) * a.K + k0 + k; };
+    auto fetch = [&](int n, int k) {
+        Eight e{};
+        if (a.accumulate && inside(n, k)) load8(e, dw, a.out_f32, place(n, k));
+        return e;
+    };
+    hand_out<S>(acc, P0, wave, lane, fetch,
+                [&](int n, int k, float *v, const float *, const Eight &e) {
+        if (!inside(n, k)) return;
+        if (a.accumulate) {
+            float o[8];
+            values8(e, a.out_f32, o);
 #pragma unroll
-    for (int j = 0; j < S::QJ; ++j) {
-        const int n = n0 + S::qrow(wq, j) + (lane & 31);
-        const size_t at0 = ((size_t)expert * a.N + n) * a.K;
-#pragma unroll
-        for (int i = 0; i < S::PI; ++i)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int k = k0 + S::prow(wp, i) + 8 * m + g4;
-                if (n >= a.N || k >= a.K) continue;
-                float v[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) v[t] = acc[i][j][4 * m + t];
-                if (a.accumulate) {
-                    float o[4];
-                    load4(dw, a.out_f32, at0 + k, o);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) v[t] += o[t];
-                }
-                store4(dw, a.out_f32, at0 + k, v);
-            }
-    }
+            for (int t = 0; t < 8; ++t) v[t] += o[t];
+        }
+        store8(dw, a.out_f32, place(n, k), v);
+    });
 }
 
 // Column sums of one row tile of bf16 rows.
 __global__ __launch_bounds__(256) void colsum_kernel(const uint16_t *__restrict__ dy, int R,
                                                      int N, const int4 *__restrict__ tiles,
                                                      const WsHeader *__restrict__ hdr,
-                                                     int max_tiles, float *__restrict__ bpart) {
+                                                     int max_tiles, int tile_rows,
+                                                     float *__restrict__ bpart) {
     const int rt = blockIdx.y, c = 2 * (blockIdx.x * 256 + threadIdx.x);
-    int rb = rt * kDenseMinTileRows, rows = min(kDenseMinTileRows, R - rb);
+    int rb = rt * tile_rows, rows = min(tile_rows, R - rb);
     if (tiles) {
         if (rt >= min(ld_const(&hdr->n_tiles), max_tiles)) return;
         const int4 tl = ld_const(tiles + rt);
@@ -293,15 +306,15 @@ __global__ __launch_bounds__(256) void colsum_kernel(const uint16_t *__restrict_
 __global__ __launch_bounds__(256) void bias_grad_kernel(const float *__restrict__ bpart,
                                                         const int32_t *__restrict__ offsets,
                                                         int R, int N, int max_tiles,
-                                                        float *__restrict__ db, int accumulate) {
+                                                        int tile_rows, float *__restrict__ db, int accumulate) {
     const int e = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
-    int first = 0, n = (R + kDenseMinTileRows - 1) / kDenseMinTileRows;
+    int first = 0, n = (R + tile_rows - 1) / tile_rows;
     if (offsets) {
         for (int i = 0; i <= e; ++i) {
             first += i ? n : 0;
             const int b = min(max(ld_const(offsets + i), 0), R);
             const int t = min(max(ld_const(offsets + i + 1), b), R);
-            n = (t - b + kDenseMinTileRows - 1) / kDenseMinTileRows;
+            n = (t - b + tile_rows - 1) / tile_rows;
         }
         first = min(first, max_tiles);
         n = min(n, max_tiles - first);
@@ -313,26 +326,53 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float *__restrict_
     db[(size_t)e * N + c] = s + sum;
 }
 
-template <DenseOp OP> hipError_t run_rows(const RowsArgs &a, hipStream_t s) {
-    using S = typename RowShape<OP>::T;
+template <DenseOp OP, bool LARGE> hipError_t run_rows(const RowsArgs &a, hipStream_t s) {
+    using S = typename RowShape<OP, LARGE>::T;
     constexpr int BC = S::DUAL ? S::BP / 2 : S::BP;
     const int ct = (a.Np + BC - 1) / BC;
     const int rt = a.tiles ? a.max_tiles : (a.R + S::BQ - 1) / S::BQ;
     const int per = a.tiles ? xcd_tile_cap(a.R, a.E, S::BQ, a.max_tiles) * ct : (rt * ct + 7) / 8;
-    rows_kernel<OP><<<8 * per, S::Threads, 0, s>>>(a, ct, rt);
+    rows_kernel<OP, LARGE><<<8 * per, S::Threads, 0, s>>>(a, ct, rt);
     return hipGetLastError();
+}
+
+template <bool LARGE> hipError_t run_grad(const GradArgs &a, hipStream_t s) {
+    using S = GradShape<LARGE>;
+    const int nt = (a.N + S::BQ - 1) / S::BQ, kt = (a.K + S::BP - 1) / S::BP;
+    const int tiles = a.E * a.mats * nt * kt;
+    grad_kernel<LARGE><<<(tiles + 7) / 8 * 8, S::Threads, 0, s>>>(a, nt, kt, tiles);
+    return hipGetLastError();
+}
+
+// Whether `large` tiles of 256 x 256 on one workgroup a CU take less time than
+// `small` ones of 128 x 128 on two.
+bool large_wins(int64_t large, int64_t small) {
+    const int cu = kCus;
+    const int64_t l = (large + cu - 1) / cu * 100;
+    const int64_t s = small <= cu ? 40 : (small + 2 * cu - 1) / (2 * cu) * 65;
+    return l <= s;
 }
 
 }  // namespace
 
+int dense_tile_rows(int R, int E, int cols, bool grouped) {
+    if (grouped) return (int64_t)R >= (int64_t)E * 256 ? 256 : 128;
+    const int64_t ct = (cols + 127) / 128;
+    return large_wins((int64_t)((R + 255) / 256) * ((cols + 255) / 256),
+                      (int64_t)((R + 127) / 128) * ct) ? 256 : 128;
+}
+
 hipError_t launch_rows(DenseOp op, const RowsArgs &a, hipStream_t s) {
+    const bool large = a.tile_rows == 256;
+#define FW_ROWS(OP) return large ? run_rows<OP, true>(a, s) : run_rows<OP, false>(a, s)
     switch (op) {
-        case kGlu: return run_rows<kGlu>(a, s);
-        case kGluGrad: return run_rows<kGluGrad>(a, s);
-        case kLinear: return run_rows<kLinear>(a, s);
-        case kLinGrad: return run_rows<kLinGrad>(a, s);
-        default: return run_rows<kInput>(a, s);
+        case kGlu: FW_ROWS(kGlu);
+        case kGluGrad: FW_ROWS(kGluGrad);
+        case kLinear: FW_ROWS(kLinear);
+        case kLinGrad: FW_ROWS(kLinGrad);
+        default: FW_ROWS(kInput);
     }
+#undef FW_ROWS
 }
 
 int64_t rows_tiles(int R, int E, int Np) {
@@ -340,39 +380,36 @@ int64_t rows_tiles(int R, int E, int Np) {
 }
 
 int64_t grad_tiles(int E, int N, int K, int mats) {
-    return (int64_t)E * mats * ((N + GradShape::BQ - 1) / GradShape::BQ) *
-           ((K + GradShape::BP - 1) / GradShape::BP);
+    return (int64_t)E * mats * ((N + 127) / 128) * ((K + 127) / 128);
 }
 
 hipError_t launch_grad(const GradArgs &a, hipStream_t s) {
-    const int nt = (a.N + GradShape::BQ - 1) / GradShape::BQ;
-    const int kt = (a.K + GradShape::BP - 1) / GradShape::BP;
-    const int tiles = a.E * a.mats * nt * kt;
-    grad_kernel<<<(tiles + 7) / 8 * 8, GradShape::Threads, 0, s>>>(a, nt, kt, tiles);
-    return hipGetLastError();
+    const bool large = large_wins((int64_t)a.E * a.mats * ((a.N + 255) / 256) * ((a.K + 255) / 256),
+                                  grad_tiles(a.E, a.N, a.K, a.mats));
+    return large ? run_grad<true>(a, s) : run_grad<false>(a, s);
 }
 
 hipError_t launch_colsum(const uint16_t *dy, int R, int N, const int4 *tiles, WsHeader *hdr,
-                         int max_tiles, float *bpart, hipStream_t s) {
-    const int rt = tiles ? max_tiles : (R + kDenseMinTileRows - 1) / kDenseMinTileRows;
+                         int max_tiles, int tile_rows, float *bpart, hipStream_t s) {
+    const int rt = tiles ? max_tiles : (R + tile_rows - 1) / tile_rows;
     colsum_kernel<<<dim3((N / 2 + 255) / 256, rt), 256, 0, s>>>(dy, R, N, tiles, hdr, max_tiles,
-                                                                bpart);
+                                                                tile_rows, bpart);
     return hipGetLastError();
 }
 
 hipError_t launch_bias_grad(const float *bpart, const int32_t *offsets, int R, int E, int N,
-                            float *db, int accumulate, hipStream_t s) {
-    const int max_tiles = (R + kDenseMinTileRows - 1) / kDenseMinTileRows + E;
-    bias_grad_kernel<<<dim3((N + 255) / 256, E), 256, 0, s>>>(bpart, offsets, R, N, max_tiles, db,
-                                                              accumulate);
+                            int max_tiles, int tile_rows, float *db, int accumulate,
+                            hipStream_t s) {
+    bias_grad_kernel<<<dim3((N + 255) / 256, E), 256, 0, s>>>(bpart, offsets, R, N, max_tiles,
+                                                              tile_rows, db, accumulate);
     return hipGetLastError();
 }
 
-hipError_t launch_dense_schedule(const int32_t *offsets, int E, int R, const DenseWs &L, char *ws,
-                                 hipStream_t s) {
+hipError_t launch_dense_schedule(const int32_t *offsets, int E, int R, int tile_rows,
+                                 const DenseWs &L, char *ws, hipStream_t s) {
     dense_schedule_kernel<<<1, kPrepThreads, 0, s>>>(
-        offsets, E, R, kDenseMinTileRows, L.max_tiles, (int4 *)(ws + L.active),
-        (int4 *)(ws + L.tiles), (int *)(ws + L.split_cnt), (WsHeader *)ws);
+        offsets, E, R, tile_rows, L.max_tiles, (int4 *)(ws + L.active), (int4 *)(ws + L.tiles),
+        (int *)(ws + L.split_cnt), (WsHeader *)ws);
     return hipGetLastError();
 }
 

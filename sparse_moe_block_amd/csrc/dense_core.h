@@ -6,9 +6,11 @@
 // Each operand is either stored along the reduction (its rows are the tile's
 // rows, "along") or across it (its rows are reduction steps, "across": weight
 // rows in dx, activation and gradient rows in dW).  Along: LDS holds [rows][64]
-// in 16-byte chunks, chunk c of row r at c ^ (r % 8), and a lane's MFMA operand
-// (row l % 32, steps 8 (l / 32) .. + 7 of a 16-step slice) is one ds_read_b128
-// whose eight-lane groups touch eight different chunk columns.  Across: LDS
+// in 16-byte chunks, chunk c of row r at c ^ (r / 2 % 8), and a lane's MFMA
+// operand (row l % 32, steps 8 (l / 32) .. + 7 of a 16-step slice) is one
+// ds_read_b128: the sixteen lanes served at once read sixteen rows, two rows to
+// a 256-byte turn of the banks, at sixteen different places in it (with
+// c ^ (r % 8) rows eight apart met: half of the LDS cycles were conflicts).  Across: LDS
 // holds [64][cols] with the 64-byte column blocks of row k moved by xor k % 4,
 // and the operand is two ds_read_b64_tr_b16, each 16-lane group reading four
 // rows x 32 bytes and receiving them transposed (four steps of one column per
@@ -18,17 +20,20 @@
 // consecutive P indices of one Q index: P is the output's contiguous dimension.
 #pragma once
 
+#include <type_traits>
+
 #include "dense.h"
 
 namespace fw {
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
-typedef float f16v __attribute__((ext_vector_type(16)));
+typedef float f4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
 constexpr int kStepK = 64;                  // reduction steps per stage
+constexpr int kSlices = kStepK / 32;        // of 32, one MFMA deep
 constexpr uint32_t kNoChunk = 0x80000000u;  // an offset beyond every range
 
 // BP x BQ tile by WP x WQ wavefronts; PX / QX: the operand is stored across.
@@ -39,15 +44,16 @@ template <int BP_, int BQ_, int WP_, int WQ_, bool PX_, bool QX_, bool DUAL_> st
     // holds the same columns of both
     static constexpr bool DUAL = DUAL_;
     static constexpr int NW = WP * WQ, Threads = 64 * NW;
-    static constexpr int PI = BP / WP / 32, QJ = BQ / WQ / 32;
+    static constexpr int PI = BP / WP / 16, QJ = BQ / WQ / 16;
     static constexpr int PChunks = BP * kStepK / 8, QChunks = BQ * kStepK / 8;
-    static_assert(!DUAL || PI == 2, "a dual tile holds one column group of each matrix");
+    static_assert(!DUAL || PI % 2 == 0, "a dual tile's wavefront holds as many groups of each matrix");
     static_assert(PChunks % Threads == 0 && QChunks % Threads == 0, "whole DMA instructions");
     // tile index of the first row of wavefront wp's P group i
     static __device__ __forceinline__ int prow(int wp, int i) {
-        return DUAL ? i * (BP / 2) + 32 * wp : wp * (BP / WP) + 32 * i;
+        return DUAL ? i / (PI / 2) * (BP / 2) + wp * (BP / 2 / WP) + 16 * (i % (PI / 2))
+                    : wp * (BP / WP) + 16 * i;
     }
-    static __device__ __forceinline__ int qrow(int wq, int j) { return wq * (BQ / WQ) + 32 * j; }
+    static __device__ __forceinline__ int qrow(int wq, int j) { return wq * (BQ / WQ) + 16 * j; }
 };
 
 // One operand as the tile sees it.  along: base = the tile's first row, `rows`
@@ -62,10 +68,14 @@ struct Operand {
 };
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
-__device__ __forceinline__ rsrc_t make_rsrc(const char *p, int64_t bytes) {
-    const int64_t n = bytes < 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes;
-    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)n, 0x00020000);
+// At most 256 rows of 131072 bytes: 32-bit lengths; none if negative.
+__device__ __forceinline__ rsrc_t make_rsrc(const char *p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, max(bytes, 0), 0x00020000);
 }
+
+// The 32-byte column block of an across operand's row is moved by xor this key:
+// the eight rows that 32 lanes read at once (r % 4, r / 8 % 2) differ in it.
+__device__ __forceinline__ int across_key(int r) { return (r & 3) | ((r >> 1) & 4); }
 
 // The DMA of one operand's stage: ROWS tile rows (columns when ACROSS), in a
 // dual tile the first half of one matrix and the second of another.
@@ -82,11 +92,11 @@ template <int ROWS, bool ACROSS, int NW, bool DUAL = false> struct Stager {
             const int idx = (i * NW + wave) * 64 + lane;
             const int r = idx / kRowChunks, p = idx % kRowChunks;
             if constexpr (ACROSS) {
-                off[i] = (uint32_t)r * pitch + 16u * (uint32_t)(p ^ ((r & 3) << 2));
+                off[i] = (uint32_t)r * pitch + 16u * (uint32_t)(p ^ (across_key(r) << 1));
             } else {
-                const int c = p ^ (r & 7);
+                const int c = p ^ ((r >> 1) & 7);
                 off[i] = (uint32_t)(DUAL ? r % (ROWS / 2) : r) * pitch + 16u * (uint32_t)c;
-                if (i == 0) kc = 8 * c;   // r % 8 = lane / 8 in every instruction
+                if (i == 0) kc = 8 * c;   // r / 2 % 8 is the same in every instruction
             }
         }
     }
@@ -94,46 +104,45 @@ template <int ROWS, bool ACROSS, int NW, bool DUAL = false> struct Stager {
     __device__ __forceinline__ rsrc_t rsrc(const Operand &o, int k, int Kd) const {
         if constexpr (ACROSS) {
             const int left = min(Kd - k, kStepK);
-            return make_rsrc(o.base + (int64_t)k * o.pitch, (int64_t)left * o.pitch - o.tail);
+            return make_rsrc(o.base + (int64_t)k * o.pitch, left * (int)o.pitch - (int)o.tail);
         } else {
-            return make_rsrc(o.base + 2 * (int64_t)k,
-                             k < Kd ? (int64_t)o.rows * o.pitch - 2 * (int64_t)k : 0);
+            return make_rsrc(o.base + 2 * (int64_t)k, k < Kd ? o.rows * (int)o.pitch - 2 * k : 0);
         }
     }
+    template <bool WHOLE>
     __device__ __forceinline__ void issue(rsrc_t r, uint4 *lds, int wave, int k, int Kd,
                                           int i) const {
-        const uint32_t o = ACROSS || k + kc < Kd ? off[i] : kNoChunk;
+        const uint32_t o = WHOLE || ACROSS || k + kc < Kd ? off[i] : kNoChunk;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(lds + (i * NW + wave) * 64), 16,
                                                  o, 0, 0, 0);
     }
 };
 
-// A lane's MFMA operands: slice s of the N groups of 32 tile rows (columns)
+// A lane's MFMA operands: slice s of the N groups of 16 tile rows (columns)
 // that start at the rows init is given.
 template <int ROWS, bool ACROSS, int N> struct Reader {
-    uint32_t at[N];            // byte offset per group
-    uint32_t in[4];            // along: the lane's chunk in a row, per slice
+    uint32_t at[N];         // byte offset per group
+    uint32_t in[kSlices];   // along: the lane's chunk in a row, per slice
     template <class F> __device__ __forceinline__ void init(int lane, F &&row0) {
+        const int q = lane >> 4, j = lane & 15;
         if constexpr (ACROSS) {
-            const int j = lane & 15, q = lane >> 4;
-            // the lane reads step 8 (q / 2) + j / 4 (+ 4), columns
-            // 16 (q % 2) + 4 (j % 4) .. + 3; its 64-byte block index is xored
-            // with step % 4 = j / 4
-            const uint32_t row = (uint32_t)(8 * (q >> 1) + (j >> 2)) * (2 * ROWS);
+            // the lane reads step 8 q + j / 4 (+ 4, + 32 s), columns 4 (j % 4) .. + 3
+            // of the group: in-group lane i then holds column i, four steps
+            const int r = 8 * q + (j >> 2);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                at[i] = row + 64u * (uint32_t)((row0(i) >> 5) ^ (j >> 2)) + 32u * (q & 1) +
-                        8u * (j & 3);
+                at[i] = (uint32_t)r * (2 * ROWS) +
+                        32u * (uint32_t)((row0(i) >> 4) ^ across_key(r)) + 8u * (j & 3);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) at[i] = 128u * (uint32_t)(row0(i) + (lane & 31));
+            for (int i = 0; i < N; ++i) at[i] = 2u * kStepK * (uint32_t)(row0(i) + j);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) in[s] = 16u * (uint32_t)((2 * s + (lane >> 5)) ^ (lane & 7));
+            for (int s = 0; s < kSlices; ++s) in[s] = 16u * (uint32_t)((4 * s + q) ^ ((j >> 1) & 7));
         }
     }
     __device__ __forceinline__ bf8 read(const uint4 *lds, int i, int s) const {
         if constexpr (ACROSS) {
-            const char *p = (const char *)lds + at[i] + (uint32_t)s * (16 * 2 * ROWS);
+            const char *p = (const char *)lds + at[i] + (uint32_t)s * (32 * 2 * ROWS);
             const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p);
             const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 4 * 2 * ROWS));
             return __builtin_bit_cast(
@@ -144,11 +153,11 @@ template <int ROWS, bool ACROSS, int N> struct Reader {
     }
 };
 
-// acc[i][j] (PI x QJ groups of 32 x 32) = the tile product over nseg segments
+// acc[i][j] (PI x QJ groups of 16 x 16) = the tile product over nseg segments
 // of Kd steps; p(seg) / pb(seg) and q(seg) give the operands (pb: the second
 // matrix of a dual P tile).
 template <class S, class PF, class PBF, class QF>
-__device__ __forceinline__ void tile_product(f16v (&acc)[S::PI][S::QJ], uint4 *P0, uint4 *P1,
+__device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], uint4 *P0, uint4 *P1,
                                              uint4 *Q0, uint4 *Q1, int wave, int lane, int Kd,
                                              int nseg, PF &&p, PBF &&pb, QF &&q) {
     const int wp = wave % S::WP, wq = wave / S::WP;
@@ -165,64 +174,167 @@ __device__ __forceinline__ void tile_product(f16v (&acc)[S::PI][S::QJ], uint4 *P
 #pragma unroll
         for (int j = 0; j < S::QJ; ++j)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.f;
 
     const int per = (Kd + kStepK - 1) / kStepK, steps = per * nseg;
     if (steps == 0) return;
-    auto load = [&](int st, uint4 *pl, uint4 *ql) {
+    // The addresses of step st's stage.  `whole`: all of its 64 reduction steps
+    // are there, which lets the DMA do without the test of each chunk; otherwise
+    // chunks outside (and past the last step everything) read as zeros.
+    struct Next {
+        rsrc_t q, p, pb;
+        int k, kd;
+    };
+    auto prepare = [&](int st) {
         const int seg = st >= per, k = (st - seg * per) * kStepK;   // nseg <= 2
-        const int kd = st < steps ? Kd : 0;   // past the end: zeros
-        const rsrc_t rq = qs.rsrc(q(seg), k, kd);
-#pragma unroll
-        for (int i = 0; i < qs.kInstr; ++i) qs.issue(rq, ql, wave, k, kd, i);
-        const rsrc_t ra = ps.rsrc(p(seg), k, kd);
-        if constexpr (S::DUAL) {
-            const rsrc_t rb = ps.rsrc(pb(seg), k, kd);
-#pragma unroll
-            for (int i = 0; i < ps.kInstr; ++i) ps.issue(2 * i < ps.kInstr ? ra : rb, pl, wave, k, kd, i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < ps.kInstr; ++i) ps.issue(ra, pl, wave, k, kd, i);
+        const int kd = st < steps ? Kd : 0;
+        return Next{qs.rsrc(q(seg), k, kd), ps.rsrc(p(seg), k, kd),
+                    S::DUAL ? ps.rsrc(pb(seg), k, kd) : ps.rsrc(p(seg), k, kd), k, kd};
+    };
+    // DMA instruction i of a stage: Q's, then P's
+    constexpr int kDma = ps.kInstr + qs.kInstr;
+    auto issue = [&](const Next &n, uint4 *pl, uint4 *ql, int i, auto whole) {
+        constexpr bool W = decltype(whole)::value;
+        if (i < qs.kInstr) {
+            qs.template issue<W>(n.q, ql, wave, n.k, n.kd, i);
+        } else if (i < kDma) {
+            const int j = i - qs.kInstr;
+            ps.template issue<W>(S::DUAL && 2 * j >= ps.kInstr ? n.pb : n.p, pl, wave, n.k, n.kd,
+                                 j);
         }
     };
-    auto step = [&](const uint4 *pl, const uint4 *ql) {
+    // The slice's operands.  P's are held twice, the next slice's read during
+    // this one; each Q operand is replaced by the next slice's right behind its
+    // MFMAs, S::QJ - 1 groups before it is needed.
+    static_assert(S::PI <= S::QJ, "one P operand read behind each group");
+    bf8 a[2][S::PI], b[S::QJ];
+    auto group = [&](int s, int j) {
 #pragma unroll
-        for (int s = 0; s < kStepK / 16; ++s) {
-            bf8 a[S::PI], b[S::QJ];
-#pragma unroll
-            for (int i = 0; i < S::PI; ++i) a[i] = pr.read(pl, i, s);
-#pragma unroll
-            for (int j = 0; j < S::QJ; ++j) b[j] = qr.read(ql, j, s);
-#pragma unroll
-            for (int i = 0; i < S::PI; ++i)
-#pragma unroll
-                for (int j = 0; j < S::QJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0,
-                                                                        0, 0);
-        }
+        for (int i = 0; i < S::PI; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][i], b[j], acc[i][j], 0, 0, 0);
     };
-    // everything issued so far has landed and every wavefront is here: the
-    // buffer read before may be refilled
+    // everything issued so far has landed and every wavefront is here
     auto sync = [&]() {
         __builtin_amdgcn_s_waitcnt(7 << 4);   // vmcnt(0) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
-    load(0, P0, Q0);
-    sync();
+    // One step: two 32-step slices.  The rendezvous comes behind the second
+    // slice's first group, when all of this buffer is in registers and its MFMAs
+    // cover the wait: from there on the reads are of the next buffer (pn, qn)
+    // and this one is refilled with step st + 2's stage, a few DMA instructions
+    // behind each group (a burst of them would fill the memory pipeline's queue
+    // and hold up the MFMAs behind it).
+    auto step = [&](int st, uint4 *pl, uint4 *ql, const uint4 *pn, const uint4 *qn, auto whole) {
+#pragma unroll
+        for (int j = 0; j < S::QJ; ++j) {
+            group(0, j);
+            b[j] = qr.read(ql, j, 1);
+            if (j < S::PI) a[1][j] = pr.read(pl, j, 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const Next n = prepare(st + 2);
+        constexpr int kPer = (kDma + S::QJ - 1) / S::QJ;
+#pragma unroll
+        for (int j = 0; j < S::QJ; ++j) {
+            group(1, j);
+            if (j == 0) sync();
+            b[j] = qr.read(qn, j, 0);
+            if (j < S::PI) a[0][j] = pr.read(pn, j, 0);
+#pragma unroll
+            for (int d = 0; d < kPer; ++d) issue(n, pl, ql, j * kPer + d, whole);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    constexpr auto whole = std::true_type{};
+    constexpr auto partial = std::false_type{};
+    Next n = prepare(0);
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) issue(n, P0, Q0, i, partial);
+    n = prepare(1);
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) issue(n, P1, Q1, i, partial);
+    __builtin_amdgcn_s_waitcnt(7 << 4 | kDma % 16 | kDma / 16 << 14);   // the first stage
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < S::PI; ++i) a[0][i] = pr.read(P0, i, 0);
+#pragma unroll
+    for (int j = 0; j < S::QJ; ++j) b[j] = qr.read(Q0, j, 0);
     // Two steps per turn, so that each buffer keeps its name (the compiler then
-    // knows that a pending DMA and a read touch different arrays).  Past the
-    // last step the loads are out of range and write zeros.
+    // knows that a pending DMA and a read touch different arrays).  The first
+    // loop's DMA is of whole stages only (step st issues stage st + 2).
     int st = 0;
-    for (; st + 1 < steps; st += 2) {
-        load(st + 1, P1, Q1);
-        step(P0, Q0);
-        sync();
-        load(st + 2, P0, Q0);
-        step(P1, Q1);
-        sync();
+    const int full = nseg == 1 || Kd % kStepK == 0 ? nseg * (Kd / kStepK) : 0;
+    for (; st + 3 < full; st += 2) {
+        step(st, P0, Q0, P1, Q1, whole);
+        step(st + 1, P1, Q1, P0, Q0, whole);
     }
-    if (st < steps) step(P0, Q0);
+    for (; st + 1 < steps; st += 2) {
+        step(st, P0, Q0, P1, Q1, partial);
+        step(st + 1, P1, Q1, P0, Q0, partial);
+    }
+    if (st < steps) step(st, P0, Q0, P1, Q1, partial);
+    // the last DMA has landed in every wavefront: the buffers are free
+    sync();
+}
+
+// Hands the accumulators out by rows: emit(row, col, v, u, e) gets eight
+// consecutive columns of one tile row (u: the same columns of a dual tile's
+// second matrix), with e = fetch(row, col) issued for half of the tile at a
+// time, ahead of its use.  Lanes of a wavefront cover whole rows of its part of
+// the tile, so loads and stores are runs of 64 or 128 bytes (16 or more) of a
+// row instead of the accumulators' 32.  The way there is LDS, 16 rows at a
+// time, private to the wavefront, the 16-byte columns of a row moved by an xor
+// of the row against bank conflicts.  lds: a buffer of the product, free again.
+template <class S> constexpr int kOutCols = S::BP / S::WP / (S::DUAL ? 2 : 1);
+
+template <class S, class Fetch, class Emit>
+__device__ __forceinline__ void hand_out(const f4 (&acc)[S::PI][S::QJ], void *lds, int wave,
+                                         int lane, Fetch &&fetch, Emit &&emit) {
+    constexpr int CW = kOutCols<S>, LR = CW / 8;   // lanes a row
+    static_assert(S::NW * (S::DUAL ? 2 : 1) * 16 * CW * 4 <= S::PChunks * 16, "LDS");
+    static_assert(CW == 64 || CW == 32, "16 or 8 columns of 16 bytes");
+    constexpr int RP = 64 / LR, NP = 16 / RP;   // rows a pass, passes per 16 rows
+    constexpr int HALF = S::QJ / 2, PG = S::DUAL ? S::PI / 2 : S::PI;
+    static_assert(RP <= 16 && S::QJ % 2 == 0, "wave tile");
+    const int wp = wave % S::WP, wq = wave / S::WP;
+    f4 *mine = (f4 *)lds + wave * (S::DUAL ? 2 : 1) * 4 * CW;
+    // 16-byte column c of row r: sixteen rows of one c, and a row's neighbours,
+    // lie in different banks
+    auto cell = [&](int r, int c) { return r * (CW / 4) + (c ^ (CW == 64 ? r : r >> 1)); };
+    const int rr = lane / LR, rc = 8 * (lane % LR);
+    const int col = wp * CW + rc;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        decltype(fetch(0, 0)) e[HALF][NP];
+#pragma unroll
+        for (int j = 0; j < HALF; ++j)
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                e[j][p] = fetch(S::qrow(wq, h * HALF + j) + p * RP + rr, col);
+#pragma unroll
+        for (int j = 0; j < HALF; ++j) {
+            const int jj = h * HALF + j;
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < S::PI; ++i)
+                mine[i / PG * 4 * CW + cell(lane & 15, 4 * (i % PG) + (lane >> 4))] = acc[i][jj];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const int lo = cell(p * RP + rr, rc / 4), hi = cell(p * RP + rr, rc / 4 + 1);
+                float v[8], u[8];
+                *(f4 *)v = mine[lo];
+                *(f4 *)(v + 4) = mine[hi];
+                if constexpr (S::DUAL) {
+                    *(f4 *)u = mine[4 * CW + lo];
+                    *(f4 *)(u + 4) = mine[4 * CW + hi];
+                }
+                emit(S::qrow(wq, jj) + p * RP + rr, col, v, u, e[j][p]);
+            }
+        }
+    }
 }
 
 }  // namespace fw
