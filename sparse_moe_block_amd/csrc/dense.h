@@ -8,7 +8,7 @@
 namespace fw {
 
 // Row tiles are at least this long, so R / kDenseMinTileRows + E bounds them.
-constexpr int kDenseMinTileRows = 128;
+constexpr int kDenseMinTileRows = 64;
 
 // Byte offsets of the scratch areas of one call inside its workspace.
 struct DenseWs {
@@ -47,7 +47,7 @@ struct RowsArgs {
     const int4 *tiles;         // row tiles, or nullptr: all R rows of expert 0
     WsHeader *hdr;
     int max_tiles;
-    int tile_rows;             // 128 or 256 (dense_tile_rows)
+    int tile_rows;             // 64, 128 or 256 (dense_tile_rows)
     const float *bias;         // [E][Np] or nullptr
     const void *residual;      // out's type, or nullptr
     const uint16_t *dy;        // bf16 [R][Np]: the arriving gradient
@@ -62,6 +62,17 @@ constexpr int kCus = 256;      // the MI355X's compute units
 int dense_tile_rows(int R, int E, int cols, bool grouped);
 hipError_t launch_rows(DenseOp op, const RowsArgs &a, hipStream_t s);
 
+// kGlu and kLinear for few rows an expert (dense_few.hip), straight from
+// offsets.  Several experts: up to 8 rows on average (128 experts, 2048 -> 1024:
+// 96 us against the tiles' 119 at 4 rows, 126 against 127 at 8, 176 against 129
+// at 16).  One matrix: up to 16 rows, and up to 32 of a long reduction, which is
+// what the tiles' time grows with (32 rows, 7168 -> 2 x 2048: 22 us against 35;
+// 2048 -> 7168: 14 us against 10.5).
+constexpr bool few_rows(int R, int E, int K) {
+    return E > 1 ? R <= 8 * E : R <= 16 || (R <= 32 && K >= 4096);
+}
+hipError_t launch_few(bool glu, const RowsArgs &a, const int32_t *offsets, hipStream_t s);
+
 // Weight gradients: dw[e][n][k] = sum over the rows r of e of dz[r][n] x[r][k].
 struct GradArgs {
     const uint16_t *dz;        // bf16 [mats][R][N]
@@ -73,7 +84,7 @@ struct GradArgs {
 };
 hipError_t launch_grad(const GradArgs &a, hipStream_t s);
 // Number of workgroups of that launch (the ABI refuses grids HIP cannot hold).
-int64_t grad_tiles(int E, int N, int K, int mats);
+int64_t grad_tiles(int E, int N, int K, int mats, int rows);
 int64_t rows_tiles(int R, int E, int Np);
 
 // db[e][n] = sum over e's rows of dz: per row tile (colsum: from bf16 rows

@@ -73,21 +73,25 @@ __device__ __forceinline__ int dense_tile(int row_tiles, int col_tiles, int &ct)
     return r0 + in % n;
 }
 
-// Tile shapes.  Large: 256 x 256, eight wavefronts of 64 x 128 outputs, one
-// workgroup a CU.  Small: 128 x 128, four wavefronts of 64 x 64, two workgroups
-// a CU.
-template <DenseOp OP, bool LARGE> struct RowShape {
-    static constexpr bool kAcross = OP == kInput, kDual = OP == kGlu || OP == kGluGrad;
-    using T = std::conditional_t<LARGE, Shape<256, 256, 4, 2, kAcross, false, kDual>,
-                                 Shape<128, 128, 2, 2, kAcross, false, kDual>>;
-};
+// Tile shapes by rows (and columns).  256: eight wavefronts of 64 x 128 outputs,
+// one workgroup a CU.  128: four wavefronts of 64 x 64, two workgroups a CU.  64:
+// four wavefronts of 32 x 32 and stages of 128 reduction steps, two workgroups a
+// CU: for products of few tiles, whose time is the number of steps.
+template <int ROWS, bool PX, bool QX, bool DUAL>
+using TileShape = std::conditional_t<
+    ROWS == 256, Shape<256, 256, 4, 2, 1, PX, QX, DUAL>,
+    std::conditional_t<ROWS == 128, Shape<128, 128, 2, 2, 1, PX, QX, DUAL>,
+                       Shape<64, 64, 2, 2, 2, PX, QX, DUAL>>>;
+template <DenseOp OP, int ROWS>
+using RowShape = TileShape<ROWS, OP == kInput, false, OP == kGlu || OP == kGluGrad>;
+template <int ROWS> constexpr int kThreads = ROWS == 256 ? 512 : 256;
+template <int ROWS> constexpr int kBlocksPerCu = ROWS == 256 ? 1 : 2;
 
 // One (row tile, column tile).
-template <DenseOp OP, bool LARGE>
-__global__ __launch_bounds__(LARGE ? 512 : 256, LARGE ? 1 : 2) void rows_kernel(RowsArgs a,
-                                                                               int col_tiles,
-                                                                               int row_tiles) {
-    using S = typename RowShape<OP, LARGE>::T;
+template <DenseOp OP, int ROWS>
+__global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void rows_kernel(
+    RowsArgs a, int col_tiles, int row_tiles) {
+    using S = RowShape<OP, ROWS>;
     __shared__ uint4 P0[S::PChunks];
     __shared__ uint4 P1[S::PChunks];
     __shared__ uint4 Q0[S::QChunks];
@@ -219,14 +223,10 @@ __global__ __launch_bounds__(LARGE ? 512 : 256, LARGE ? 1 : 2) void rows_kernel(
 }
 
 // dw tiles: Q = output features (rows of dw), P = input features.
-template <bool LARGE>
-using GradShape = std::conditional_t<LARGE, Shape<256, 256, 4, 2, true, true, false>,
-                                     Shape<128, 128, 2, 2, true, true, false>>;
-
-template <bool LARGE>
-__global__ __launch_bounds__(LARGE ? 512 : 256, LARGE ? 1 : 2) void grad_kernel(GradArgs a, int nt,
-                                                                               int kt, int tiles) {
-    using S = GradShape<LARGE>;
+template <int ROWS>
+__global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void grad_kernel(
+    GradArgs a, int nt, int kt, int tiles) {
+    using S = TileShape<ROWS, true, true, false>;
     __shared__ uint4 P0[S::PChunks];
     __shared__ uint4 P1[S::PChunks];
     __shared__ uint4 Q0[S::QChunks];
@@ -276,13 +276,16 @@ __global__ __launch_bounds__(LARGE ? 512 : 256, LARGE ? 1 : 2) void grad_kernel(
     });
 }
 
-// Column sums of one row tile of bf16 rows.
+// Column sums of one row tile of bf16 rows: a workgroup takes 64 columns,
+// eight lanes (16 bytes each) a row and 32 rows at a time, so that the rows'
+// loads are in flight together; the 32 partial sums meet in LDS, in order.
 __global__ __launch_bounds__(256) void colsum_kernel(const uint16_t *__restrict__ dy, int R,
                                                      int N, const int4 *__restrict__ tiles,
                                                      const WsHeader *__restrict__ hdr,
                                                      int max_tiles, int tile_rows,
                                                      float *__restrict__ bpart) {
-    const int rt = blockIdx.y, c = 2 * (blockIdx.x * 256 + threadIdx.x);
+    __shared__ float part[32][64];
+    const int rt = blockIdx.y, c0 = blockIdx.x * 64;
     int rb = rt * tile_rows, rows = min(tile_rows, R - rb);
     if (tiles) {
         if (rt >= min(ld_const(&hdr->n_tiles), max_tiles)) return;
@@ -290,15 +293,30 @@ __global__ __launch_bounds__(256) void colsum_kernel(const uint16_t *__restrict_
         rb = tl.y;
         rows = tl.z;
     }
-    if (c >= N) return;
-    float s0 = 0.f, s1 = 0.f;
-    const uint16_t *p = dy + (size_t)rb * N + c;
-    for (int r = 0; r < rows; ++r, p += N) {
-        const uint32_t v = *(const uint32_t *)p;
-        s0 += bf16_lo(v);
-        s1 += bf16_hi(v);
+    const int c = 8 * (threadIdx.x % 8), r0 = threadIdx.x / 8;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c0 + c < N) {
+        const uint16_t *p = dy + (size_t)rb * N + c0 + c;
+#pragma unroll 4
+        for (int r = r0; r < rows; r += 32) {
+            Eight e;
+            float v[8];
+            load8(e, p, 0, (size_t)r * N);
+            e.r[1] = uint4{0, 0, 0, 0};
+            values8(e, 0, v);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) s[t] += v[t];
+        }
     }
-    *(float2 *)(bpart + (size_t)rt * N + c) = float2{s0, s1};
+#pragma unroll
+    for (int t = 0; t < 8; ++t) part[r0][c + t] = s[t];
+    __syncthreads();
+    if (threadIdx.x < 64 && c0 + (int)threadIdx.x < N) {
+        float sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) sum += part[r][threadIdx.x];
+        bpart[(size_t)rt * N + c0 + threadIdx.x] = sum;
+    }
 }
 
 // db[e] = the sum of e's row tiles' partials, in tile order (the schedule
@@ -306,93 +324,108 @@ __global__ __launch_bounds__(256) void colsum_kernel(const uint16_t *__restrict_
 __global__ __launch_bounds__(256) void bias_grad_kernel(const float *__restrict__ bpart,
                                                         const int32_t *__restrict__ offsets,
                                                         int R, int N, int max_tiles,
-                                                        int tile_rows, float *__restrict__ db, int accumulate) {
+                                                        int tile_rows, float *__restrict__ db,
+                                                        int accumulate) {
+    __shared__ int before[256], own;
     const int e = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
     int first = 0, n = (R + tile_rows - 1) / tile_rows;
     if (offsets) {
-        for (int i = 0; i <= e; ++i) {
-            first += i ? n : 0;
-            const int b = min(max(ld_const(offsets + i), 0), R);
-            const int t = min(max(ld_const(offsets + i + 1), b), R);
-            n = (t - b + tile_rows - 1) / tile_rows;
+        int mine = 0;
+        for (int i = threadIdx.x; i <= e; i += 256) {
+            const int b = min(max(offsets[i], 0), R), t = min(max(offsets[i + 1], b), R);
+            const int nt = (t - b + tile_rows - 1) / tile_rows;
+            if (i == e) own = nt;
+            else mine += nt;
         }
-        first = min(first, max_tiles);
-        n = min(n, max_tiles - first);
+        before[threadIdx.x] = mine;
+        __syncthreads();
+        for (int o = 128; o > 0; o >>= 1) {
+            if ((int)threadIdx.x < o) before[threadIdx.x] += before[threadIdx.x + o];
+            __syncthreads();
+        }
+        first = min(before[0], max_tiles);
+        n = min(own, max_tiles - first);
     }
     if (c >= N) return;
-    float s = accumulate ? db[(size_t)e * N + c] : 0.f;
+    const float s = accumulate ? db[(size_t)e * N + c] : 0.f;
+    const float *p = bpart + (size_t)first * N + c;
     float sum = 0.f;
-    for (int i = 0; i < n; ++i) sum += bpart[(size_t)(first + i) * N + c];
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) sum += p[(size_t)i * N];
     db[(size_t)e * N + c] = s + sum;
 }
 
-template <DenseOp OP, bool LARGE> hipError_t run_rows(const RowsArgs &a, hipStream_t s) {
-    using S = typename RowShape<OP, LARGE>::T;
+template <DenseOp OP, int ROWS> hipError_t run_rows(const RowsArgs &a, hipStream_t s) {
+    using S = RowShape<OP, ROWS>;
     constexpr int BC = S::DUAL ? S::BP / 2 : S::BP;
     const int ct = (a.Np + BC - 1) / BC;
     const int rt = a.tiles ? a.max_tiles : (a.R + S::BQ - 1) / S::BQ;
     const int per = a.tiles ? xcd_tile_cap(a.R, a.E, S::BQ, a.max_tiles) * ct : (rt * ct + 7) / 8;
-    rows_kernel<OP, LARGE><<<8 * per, S::Threads, 0, s>>>(a, ct, rt);
+    rows_kernel<OP, ROWS><<<8 * per, S::Threads, 0, s>>>(a, ct, rt);
     return hipGetLastError();
 }
+template <DenseOp OP> hipError_t pick_rows(const RowsArgs &a, hipStream_t s) {
+    return a.tile_rows == 256   ? run_rows<OP, 256>(a, s)
+           : a.tile_rows == 128 ? run_rows<OP, 128>(a, s)
+                                : run_rows<OP, 64>(a, s);
+}
 
-template <bool LARGE> hipError_t run_grad(const GradArgs &a, hipStream_t s) {
-    using S = GradShape<LARGE>;
-    const int nt = (a.N + S::BQ - 1) / S::BQ, kt = (a.K + S::BP - 1) / S::BP;
+template <int ROWS> hipError_t run_grad(const GradArgs &a, hipStream_t s) {
+    const int nt = (a.N + ROWS - 1) / ROWS, kt = (a.K + ROWS - 1) / ROWS;
     const int tiles = a.E * a.mats * nt * kt;
-    grad_kernel<LARGE><<<(tiles + 7) / 8 * 8, S::Threads, 0, s>>>(a, nt, kt, tiles);
+    grad_kernel<ROWS><<<(tiles + 7) / 8 * 8, kThreads<ROWS>, 0, s>>>(a, nt, kt, tiles);
     return hipGetLastError();
 }
 
-// Whether `large` tiles of 256 x 256 on one workgroup a CU take less time than
-// `small` ones of 128 x 128 on two.
-bool large_wins(int64_t large, int64_t small) {
-    const int cu = kCus;
-    const int64_t l = (large + cu - 1) / cu * 100;
-    const int64_t s = small <= cu ? 40 : (small + 2 * cu - 1) / (2 * cu) * 65;
-    return l <= s;
+// The tile shape that takes the least time for `tiles(rows)` tiles, in percent
+// of a round of 256-row tiles.  Measured: 2048 x 4096 -> 1536 in 89 us with 48
+// tiles of 256, 48 us with 192 of 128 (one a CU); 4096 x 7168 -> 2048 in 150 us
+// with 128 tiles of 256, 119 us with 512 of 128 (two a CU); 777 x 4096 -> 1536
+// in 38 us with 84 tiles of 128, 26 us with 312 of 64; 777 x 1536 -> 4096 in 25
+// us with 224 tiles of 128, 28 us with 832 of 64.
+template <class F> int best_tile(F &&tiles) {
+    const int64_t large = tiles(256), small = tiles(128), tiny = tiles(64);
+    auto rounds = [](int64_t n, int64_t per) { return (n + per - 1) / per; };
+    const int64_t l = rounds(large, kCus) * 100;
+    const int64_t s = small <= kCus ? 45 : rounds(small, 2 * kCus) * 65;
+    const int64_t t = rounds(tiny, 2 * kCus) * 31;
+    return l <= s && l <= t ? 256 : s <= t ? 128 : 64;
 }
 
 }  // namespace
 
 int dense_tile_rows(int R, int E, int cols, bool grouped) {
-    if (grouped) return (int64_t)R >= (int64_t)E * 256 ? 256 : 128;
-    const int64_t ct = (cols + 127) / 128;
-    return large_wins((int64_t)((R + 255) / 256) * ((cols + 255) / 256),
-                      (int64_t)((R + 127) / 128) * ct) ? 256 : 128;
+    if (grouped) return R >= E * 256LL ? 256 : R >= E * 64LL ? 128 : 64;
+    return best_tile([&](int r) { return (int64_t)((R + r - 1) / r) * ((cols + r - 1) / r); });
 }
 
 hipError_t launch_rows(DenseOp op, const RowsArgs &a, hipStream_t s) {
-    const bool large = a.tile_rows == 256;
-#define FW_ROWS(OP) return large ? run_rows<OP, true>(a, s) : run_rows<OP, false>(a, s)
     switch (op) {
-        case kGlu: FW_ROWS(kGlu);
-        case kGluGrad: FW_ROWS(kGluGrad);
-        case kLinear: FW_ROWS(kLinear);
-        case kLinGrad: FW_ROWS(kLinGrad);
-        default: FW_ROWS(kInput);
+        case kGlu: return pick_rows<kGlu>(a, s);
+        case kGluGrad: return pick_rows<kGluGrad>(a, s);
+        case kLinear: return pick_rows<kLinear>(a, s);
+        case kLinGrad: return pick_rows<kLinGrad>(a, s);
+        default: return pick_rows<kInput>(a, s);
     }
-#undef FW_ROWS
 }
 
 int64_t rows_tiles(int R, int E, int Np) {
-    return (int64_t)((R + 127) / 128 + E + 8) * ((Np + 63) / 64);
+    return (int64_t)((R + 63) / 64 + E + 8) * ((Np + 31) / 32);
 }
 
-int64_t grad_tiles(int E, int N, int K, int mats) {
-    return (int64_t)E * mats * ((N + 127) / 128) * ((K + 127) / 128);
+int64_t grad_tiles(int E, int N, int K, int mats, int rows) {
+    return (int64_t)E * mats * ((N + rows - 1) / rows) * ((K + rows - 1) / rows);
 }
 
 hipError_t launch_grad(const GradArgs &a, hipStream_t s) {
-    const bool large = large_wins((int64_t)a.E * a.mats * ((a.N + 255) / 256) * ((a.K + 255) / 256),
-                                  grad_tiles(a.E, a.N, a.K, a.mats));
-    return large ? run_grad<true>(a, s) : run_grad<false>(a, s);
+    const int rows = best_tile([&](int r) { return grad_tiles(a.E, a.N, a.K, a.mats, r); });
+    return rows == 256 ? run_grad<256>(a, s) : rows == 128 ? run_grad<128>(a, s) : run_grad<64>(a, s);
 }
 
 hipError_t launch_colsum(const uint16_t *dy, int R, int N, const int4 *tiles, WsHeader *hdr,
                          int max_tiles, int tile_rows, float *bpart, hipStream_t s) {
     const int rt = tiles ? max_tiles : (R + tile_rows - 1) / tile_rows;
-    colsum_kernel<<<dim3((N / 2 + 255) / 256, rt), 256, 0, s>>>(dy, R, N, tiles, hdr, max_tiles,
+    colsum_kernel<<<dim3((N + 63) / 64, rt), 256, 0, s>>>(dy, R, N, tiles, hdr, max_tiles,
                                                                 tile_rows, bpart);
     return hipGetLastError();
 }

@@ -55,7 +55,7 @@ int check_dense(const fw_moe_dense_desc *d) {
     if (!dtype_ok(d->out_dtype) || !dtype_ok(d->grad_dtype)) return FW_EINVAL;
     if (d->accumulate != 0 && d->accumulate != 1) return FW_EINVAL;
     if (d->ckpt != FW_ACT_NONE && d->in_features % 32) return FW_EUNSUPPORTED;
-    if (!grid_ok(grad_tiles(d->n_experts, d->out_features, d->in_features, 2))) return FW_EINVAL;
+    if (!grid_ok(grad_tiles(d->n_experts, d->out_features, d->in_features, 2, 128))) return FW_EINVAL;
     return FW_OK;
 }
 
@@ -103,6 +103,7 @@ struct Call {
     int tile_rows(int cols) const {
         return dense_tile_rows(R, d.n_experts, cols, offsets != nullptr);
     }
+    bool few() const { return few_rows(R, d.n_experts, d.in_features); }
     const int4 *tiles() const { return offsets ? (const int4 *)(ws + L.tiles) : nullptr; }
     // forward-shaped product: x [R][K] times weights [N][K]
     RowsArgs rows(const void *x, const void *w0, const void *w1) const {
@@ -182,10 +183,11 @@ int fw_moe_glu_forward(const fw_moe_dense_desc *desc, int32_t R, const void *x,
     rc = check_call(desc, R, expert_offsets, {x, w_gate, w_up, h}, {}, workspace, ws_bytes);
     if (rc != FW_OK) return rc;
     const Call c(*desc, R, expert_offsets, workspace, stream);
-    if ((rc = c.schedule()) != FW_OK) return rc;
     RowsArgs a = c.rows(x, w_gate, w_up);
     a.out = h;
     a.out_f32 = desc->out_dtype == FW_F32;
+    if (c.few()) return hip_status(launch_few(true, a, expert_offsets, c.s));
+    if ((rc = c.schedule()) != FW_OK) return rc;
     return hip_status(launch_rows(kGlu, a, c.s));
 }
 
@@ -229,12 +231,13 @@ int fw_moe_linear_forward(const fw_moe_dense_desc *desc, int32_t R, const void *
     rc = check_call(desc, R, expert_offsets, {x, w, y}, {bias, residual}, workspace, ws_bytes);
     if (rc != FW_OK) return rc;
     const Call c(*desc, R, expert_offsets, workspace, stream);
-    if ((rc = c.schedule()) != FW_OK) return rc;
     RowsArgs a = c.rows(x, w, nullptr);
     a.bias = bias;
     a.residual = residual;
     a.out = y;
     a.out_f32 = desc->out_dtype == FW_F32;
+    if (c.few()) return hip_status(launch_few(false, a, expert_offsets, c.s));
+    if ((rc = c.schedule()) != FW_OK) return rc;
     return hip_status(launch_rows(kLinear, a, c.s));
 }
 

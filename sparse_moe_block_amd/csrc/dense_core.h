@@ -32,22 +32,26 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
-constexpr int kStepK = 64;                  // reduction steps per stage
+constexpr int kStepK = 64;                  // reduction steps per block of a stage
 constexpr int kSlices = kStepK / 32;        // of 32, one MFMA deep
 constexpr uint32_t kNoChunk = 0x80000000u;  // an offset beyond every range
 
-// BP x BQ tile by WP x WQ wavefronts; PX / QX: the operand is stored across.
-template <int BP_, int BQ_, int WP_, int WQ_, bool PX_, bool QX_, bool DUAL_> struct Shape {
-    static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_;
+// BP x BQ tile by WP x WQ wavefronts, D blocks of 64 steps a stage; PX / QX: the
+// operand is stored across.
+template <int BP_, int BQ_, int WP_, int WQ_, int D_, bool PX_, bool QX_, bool DUAL_>
+struct Shape {
+    static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, D = D_;
     static constexpr bool PX = PX_, QX = QX_;
     // the P tile is half of one matrix and half of another, so that a wavefront
     // holds the same columns of both
     static constexpr bool DUAL = DUAL_;
     static constexpr int NW = WP * WQ, Threads = 64 * NW;
     static constexpr int PI = BP / WP / 16, QJ = BQ / WQ / 16;
-    static constexpr int PChunks = BP * kStepK / 8, QChunks = BQ * kStepK / 8;
+    // 16-byte chunks of a stage
+    static constexpr int PChunks = D * BP * kStepK / 8, QChunks = D * BQ * kStepK / 8;
     static_assert(!DUAL || PI % 2 == 0, "a dual tile's wavefront holds as many groups of each matrix");
-    static_assert(PChunks % Threads == 0 && QChunks % Threads == 0, "whole DMA instructions");
+    static_assert(PChunks % (D * Threads) == 0 && QChunks % (D * Threads) == 0,
+                  "whole DMA instructions");
     // tile index of the first row of wavefront wp's P group i
     static __device__ __forceinline__ int prow(int wp, int i) {
         return DUAL ? i / (PI / 2) * (BP / 2) + wp * (BP / 2 / WP) + 16 * (i % (PI / 2))
@@ -74,13 +78,16 @@ __device__ __forceinline__ rsrc_t make_rsrc(const char *p, int bytes) {
 }
 
 // The 32-byte column block of an across operand's row is moved by xor this key:
-// the eight rows that 32 lanes read at once (r % 4, r / 8 % 2) differ in it.
-__device__ __forceinline__ int across_key(int r) { return (r & 3) | ((r >> 1) & 4); }
+// the eight rows that 32 lanes read at once (r % 4, r / 8 % 2) differ in it, or,
+// in rows of 64 columns (two to a turn of the banks), four pairs of them do.
+template <int ROWS> __device__ __forceinline__ int across_key(int r) {
+    return ROWS >= 128 ? (r & 3) | ((r >> 1) & 4) : ((r >> 1) & 1) | ((r >> 2) & 2);
+}
 
 // The DMA of one operand's stage: ROWS tile rows (columns when ACROSS), in a
 // dual tile the first half of one matrix and the second of another.
 template <int ROWS, bool ACROSS, int NW, bool DUAL = false> struct Stager {
-    static_assert(!ACROSS || (ROWS >= 128 && !DUAL), "four 64-byte blocks to permute");
+    static_assert(!ACROSS || (ROWS >= 128 && !DUAL) || ROWS == 64, "whole column blocks");
     static constexpr int kInstr = ROWS * kStepK / 8 / (64 * NW);
     static constexpr int kRowChunks = ACROSS ? ROWS / 8 : kStepK / 8;
     uint32_t off[kInstr];
@@ -92,7 +99,7 @@ template <int ROWS, bool ACROSS, int NW, bool DUAL = false> struct Stager {
             const int idx = (i * NW + wave) * 64 + lane;
             const int r = idx / kRowChunks, p = idx % kRowChunks;
             if constexpr (ACROSS) {
-                off[i] = (uint32_t)r * pitch + 16u * (uint32_t)(p ^ (across_key(r) << 1));
+                off[i] = (uint32_t)r * pitch + 16u * (uint32_t)(p ^ (across_key<ROWS>(r) << 1));
             } else {
                 const int c = p ^ ((r >> 1) & 7);
                 off[i] = (uint32_t)(DUAL ? r % (ROWS / 2) : r) * pitch + 16u * (uint32_t)c;
@@ -132,7 +139,7 @@ template <int ROWS, bool ACROSS, int N> struct Reader {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 at[i] = (uint32_t)r * (2 * ROWS) +
-                        32u * (uint32_t)((row0(i) >> 4) ^ across_key(r)) + 8u * (j & 3);
+                        32u * (uint32_t)((row0(i) >> 4) ^ across_key<ROWS>(r)) + 8u * (j & 3);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) at[i] = 2u * kStepK * (uint32_t)(row0(i) + j);
@@ -176,31 +183,41 @@ __device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], uint4 *P0,
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.f;
 
-    const int per = (Kd + kStepK - 1) / kStepK, steps = per * nseg;
+    constexpr int kStage = S::D * kStepK;
+    const int per = (Kd + kStage - 1) / kStage, steps = per * nseg;
     if (steps == 0) return;
     // The addresses of step st's stage.  `whole`: all of its 64 reduction steps
     // are there, which lets the DMA do without the test of each chunk; otherwise
     // chunks outside (and past the last step everything) read as zeros.
     struct Next {
-        rsrc_t q, p, pb;
+        rsrc_t q[S::D], p[S::D], pb[S::DUAL ? S::D : 1];
         int k, kd;
     };
     auto prepare = [&](int st) {
-        const int seg = st >= per, k = (st - seg * per) * kStepK;   // nseg <= 2
-        const int kd = st < steps ? Kd : 0;
-        return Next{qs.rsrc(q(seg), k, kd), ps.rsrc(p(seg), k, kd),
-                    S::DUAL ? ps.rsrc(pb(seg), k, kd) : ps.rsrc(p(seg), k, kd), k, kd};
+        Next n;
+        const int seg = st >= per;   // nseg <= 2
+        n.k = (st - seg * per) * kStage;
+        n.kd = st < steps ? Kd : 0;
+#pragma unroll
+        for (int d = 0; d < S::D; ++d) {
+            n.q[d] = qs.rsrc(q(seg), n.k + d * kStepK, n.kd);
+            n.p[d] = ps.rsrc(p(seg), n.k + d * kStepK, n.kd);
+            if constexpr (S::DUAL) n.pb[d] = ps.rsrc(pb(seg), n.k + d * kStepK, n.kd);
+        }
+        return n;
     };
-    // DMA instruction i of a stage: Q's, then P's
-    constexpr int kDma = ps.kInstr + qs.kInstr;
+    // DMA instruction i of a stage: per block Q's, then P's
+    constexpr int kBlockDma = ps.kInstr + qs.kInstr, kDma = S::D * kBlockDma;
     auto issue = [&](const Next &n, uint4 *pl, uint4 *ql, int i, auto whole) {
         constexpr bool W = decltype(whole)::value;
-        if (i < qs.kInstr) {
-            qs.template issue<W>(n.q, ql, wave, n.k, n.kd, i);
-        } else if (i < kDma) {
-            const int j = i - qs.kInstr;
-            ps.template issue<W>(S::DUAL && 2 * j >= ps.kInstr ? n.pb : n.p, pl, wave, n.k, n.kd,
-                                 j);
+        if (i >= kDma) return;
+        const int d = i / kBlockDma, j = i % kBlockDma, k = n.k + d * kStepK;
+        if (j < qs.kInstr) {
+            qs.template issue<W>(n.q[d], ql + d * (S::QChunks / S::D), wave, k, n.kd, j);
+        } else {
+            const int m = j - qs.kInstr;
+            ps.template issue<W>(S::DUAL && 2 * m >= ps.kInstr ? n.pb[S::DUAL ? d : 0] : n.p[d],
+                                 pl + d * (S::PChunks / S::D), wave, k, n.kd, m);
         }
     };
     // The slice's operands.  P's are held twice, the next slice's read during
@@ -219,32 +236,36 @@ __device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], uint4 *P0,
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
-    // One step: two 32-step slices.  The rendezvous comes behind the second
+    // One step: the stage's 32-step slices.  The rendezvous comes behind the last
     // slice's first group, when all of this buffer is in registers and its MFMAs
     // cover the wait: from there on the reads are of the next buffer (pn, qn)
     // and this one is refilled with step st + 2's stage, a few DMA instructions
     // behind each group (a burst of them would fill the memory pipeline's queue
     // and hold up the MFMAs behind it).
+    constexpr int kAll = S::D * kSlices;
+    auto slice = [&](int x, const uint4 *pl, const uint4 *ql, int s, auto &&behind) {
+        // reads slice s of (pl, ql) while the present one's MFMAs run
+        const uint4 *pd = pl + s / kSlices * (S::PChunks / S::D);
+        const uint4 *qd = ql + s / kSlices * (S::QChunks / S::D);
+#pragma unroll
+        for (int j = 0; j < S::QJ; ++j) {
+            group(x, j);
+            behind(j);
+            b[j] = qr.read(qd, j, s % kSlices);
+            if (j < S::PI) a[x ^ 1][j] = pr.read(pd, j, s % kSlices);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
     auto step = [&](int st, uint4 *pl, uint4 *ql, const uint4 *pn, const uint4 *qn, auto whole) {
 #pragma unroll
-        for (int j = 0; j < S::QJ; ++j) {
-            group(0, j);
-            b[j] = qr.read(ql, j, 1);
-            if (j < S::PI) a[1][j] = pr.read(pl, j, 1);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int s = 0; s + 1 < kAll; ++s) slice(s & 1, pl, ql, s + 1, [](int) {});
         const Next n = prepare(st + 2);
         constexpr int kPer = (kDma + S::QJ - 1) / S::QJ;
-#pragma unroll
-        for (int j = 0; j < S::QJ; ++j) {
-            group(1, j);
+        slice((kAll - 1) & 1, pn, qn, 0, [&](int j) {
             if (j == 0) sync();
-            b[j] = qr.read(qn, j, 0);
-            if (j < S::PI) a[0][j] = pr.read(pn, j, 0);
 #pragma unroll
             for (int d = 0; d < kPer; ++d) issue(n, pl, ql, j * kPer + d, whole);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        });
     };
     constexpr auto whole = std::true_type{};
     constexpr auto partial = std::false_type{};
@@ -265,7 +286,7 @@ __device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], uint4 *P0,
     // knows that a pending DMA and a read touch different arrays).  The first
     // loop's DMA is of whole stages only (step st issues stage st + 2).
     int st = 0;
-    const int full = nseg == 1 || Kd % kStepK == 0 ? nseg * (Kd / kStepK) : 0;
+    const int full = nseg == 1 || Kd % kStage == 0 ? nseg * (Kd / kStage) : 0;
     for (; st + 3 < full; st += 2) {
         step(st, P0, Q0, P1, Q1, whole);
         step(st + 1, P1, Q1, P0, Q0, whole);
@@ -294,16 +315,20 @@ __device__ __forceinline__ void hand_out(const f4 (&acc)[S::PI][S::QJ], void *ld
                                          int lane, Fetch &&fetch, Emit &&emit) {
     constexpr int CW = kOutCols<S>, LR = CW / 8;   // lanes a row
     static_assert(S::NW * (S::DUAL ? 2 : 1) * 16 * CW * 4 <= S::PChunks * 16, "LDS");
-    static_assert(CW == 64 || CW == 32, "16 or 8 columns of 16 bytes");
-    constexpr int RP = 64 / LR, NP = 16 / RP;   // rows a pass, passes per 16 rows
+    static_assert(CW == 64 || CW == 32 || CW == 16, "4, 8 or 16 columns of 16 bytes");
+    // rows a pass, passes per 16 rows (16 columns: half of the lanes have a row)
+    constexpr int RP = LR < 4 ? 16 : 64 / LR, NP = 16 / RP;
     constexpr int HALF = S::QJ / 2, PG = S::DUAL ? S::PI / 2 : S::PI;
     static_assert(RP <= 16 && S::QJ % 2 == 0, "wave tile");
     const int wp = wave % S::WP, wq = wave / S::WP;
     f4 *mine = (f4 *)lds + wave * (S::DUAL ? 2 : 1) * 4 * CW;
     // 16-byte column c of row r: sixteen rows of one c, and a row's neighbours,
     // lie in different banks
-    auto cell = [&](int r, int c) { return r * (CW / 4) + (c ^ (CW == 64 ? r : r >> 1)); };
-    const int rr = lane / LR, rc = 8 * (lane % LR);
+    auto cell = [&](int r, int c) {
+        return r * (CW / 4) + (c ^ (CW == 64 ? r : CW == 32 ? r >> 1 : r >> 2));
+    };
+    const int rr = lane / LR % RP, rc = 8 * (lane % LR);
+    const bool idle = lane / LR >= RP;
     const int col = wp * CW + rc;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -312,7 +337,7 @@ __device__ __forceinline__ void hand_out(const f4 (&acc)[S::PI][S::QJ], void *ld
         for (int j = 0; j < HALF; ++j)
 #pragma unroll
             for (int p = 0; p < NP; ++p)
-                e[j][p] = fetch(S::qrow(wq, h * HALF + j) + p * RP + rr, col);
+                if (!idle) e[j][p] = fetch(S::qrow(wq, h * HALF + j) + p * RP + rr, col);
 #pragma unroll
         for (int j = 0; j < HALF; ++j) {
             const int jj = h * HALF + j;
@@ -331,7 +356,7 @@ __device__ __forceinline__ void hand_out(const f4 (&acc)[S::PI][S::QJ], void *ld
                     *(f4 *)u = mine[4 * CW + lo];
                     *(f4 *)(u + 4) = mine[4 * CW + hi];
                 }
-                emit(S::qrow(wq, jj) + p * RP + rr, col, v, u, e[j][p]);
+                if (!idle) emit(S::qrow(wq, jj) + p * RP + rr, col, v, u, e[j][p]);
             }
         }
     }

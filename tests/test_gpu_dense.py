@@ -22,8 +22,9 @@ SHAPES = [
     (17, 200, 264, None), (33, 520, 40, None), (64, 1032, 72, None), (127, 96, 392, None),
     (128, 128, 128, None), (129, 64, 520, None), (257, 328, 200, None), (300, 136, 1032, None),
     (5, 64, 136, [0, 3]), (200, 96, 136, [0, 131, 200]), (70, 72, 88, [0, 0, 64, 64, 65, 69]),
-    (777, 72, 1032, None), (1400, 40, 136, [0, 700, 700, 1390]), (9, 264, 40, [0, 1, 2, 3, 4, 5, 6, 7, 8, 9]), (40, 40, 64, [0, 0, 0, 0]),
+    (20, 4104, 40, None), (31, 4128, 24, [0, 29]), (777, 72, 1032, None), (1400, 40, 136, [0, 700, 700, 1390]), (9, 264, 40, [0, 1, 2, 3, 4, 5, 6, 7, 8, 9]), (40, 40, 64, [0, 0, 0, 0]),
     (520, 136, 72, [0, 1, 259, 259, 400, 519]), (300, 64, 24, [0, 0, 300, 300]),
+    (60, 296, 40, [0, 33, 33, 34, 34, 34, 34, 34, 51, 59]),
 ]
 IDS = [f"{r}x{k}x{n}" + ("" if o is None else f"e{len(o) - 1}") for r, k, n, o in SHAPES]
 
