@@ -264,62 +264,75 @@ def fw_moe_layer_noalloc(desc, T, x, router_w, logit_bias, w_gate, w_up, w_down,
 # The kernels read flat row-major memory: a tensor of another size, type or
 # layout, or on another device than the rest, is refused here (ValueError)
 # before the library sees its pointer.  Raw integer pointers pass unchecked.
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+# Decode-sized calls take about as long on the host as on the GPU, hence the
+# plain loops.
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _OUT = {FW_F32: _F32, FW_BF16: _BF16}
 # element types of a checkpoint's codes and scales
 _CODES = {FW_ACT_MXFP8: ((torch.uint8, torch.float8_e4m3fn), (torch.uint8,)),
-          FW_ACT_INT8: ((torch.int8, torch.uint8), (_F32,))}
+          FW_ACT_INT8: ((torch.int8, torch.uint8), _F32)}
 
 
-def _operand(fn, name, t, count, dtypes, device):
-    """Check one tensor argument (None and raw pointers pass); its device."""
-    if t is None or isinstance(t, int):
-        return device
+def _refuse(fn, name, t, count, dtypes, device):
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} is {t.dtype}, not {' or '.join(map(str, dtypes))}")
     if t.numel() != count:
         raise ValueError(f"{fn}: {name} has {t.numel()} elements, not {count}")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{fn}: {name} is on {t.device}, not {device}")
-    return t.device
+    raise ValueError(f"{fn}: {name} is on {t.device}, not on " +
+                     ("a GPU" if device < 0 else f"cuda:{device} like the others"))
 
 
-def _launch(fn, operands, workspace, ws_bytes, stream, call):
-    """Check the operands (name, tensor, elements, types), then call(workspace
-    bytes, stream) with their device current."""
+def _call(fn, desc, R, operands, args, workspace, ws_bytes, stream):
+    """Check the operands (name, tensor or None, elements, types), then call
+    the library's fn(desc, R, *args, [workspace, [its bytes,]] stream) with
+    their device current."""
     device = None
     for name, t, count, dtypes in operands:
-        device = _operand(fn, name, t, count, dtypes, device)
-    if ws_bytes is None and workspace is not None:
-        device = _operand(fn, "workspace", workspace, workspace.numel(), (workspace.dtype,),
-                          device)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    if device is not None and device.type != "cuda":
-        raise ValueError(f"{fn}: tensors are on {device}, not on a GPU")
-    if device is None or device.index == torch.cuda.current_device():
-        return _check(fn, call(ws_bytes or 0, _stream(stream)))
-    with torch.cuda.device(device):
-        return _check(fn, call(ws_bytes or 0, _stream(stream)))
-
-
-def _sizes(desc, R):
-    K, N, E = desc.in_features, desc.out_features, desc.n_experts
-    return R * K, R * N, E * N * K, E * N
+        if t is None or type(t) is int:
+            continue
+        d = t.get_device()
+        if device is None:
+            device, first = d, (name, t, count, dtypes)
+        if (d != device or t.dtype not in dtypes or t.numel() != count or
+                not t.is_contiguous()):
+            _refuse(fn, name, t, count, dtypes, device)
+    if device is not None and device < 0:
+        _refuse(fn, *first, device)
+    tail = []
+    if workspace is not None:
+        ws, sized = workspace
+        if ws is not None and type(ws) is not int:
+            if ws.get_device() != device is not None or not ws.is_contiguous():
+                _refuse(fn, "workspace", ws, ws.numel(), (ws.dtype,), device)
+            if ws_bytes is None:
+                ws_bytes = ws.numel() * ws.element_size()
+            ws = ws.data_ptr()
+        tail = [ws, ws_bytes or 0] if sized else [ws]
+    here = torch.cuda.current_device()
+    elsewhere = device is not None and device != here
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device if elsewhere else here)
+    else:
+        stream = _stream(stream)
+    f = getattr(_lib or lib(), fn)
+    ptrs = [t if t is None or type(t) is int else t.data_ptr() for t in args]
+    if elsewhere:
+        with torch.cuda.device(device):
+            rc = f(desc, R, *ptrs, *tail, stream)
+    else:
+        rc = f(desc, R, *ptrs, *tail, stream)
+    return rc if rc == FW_OK else _check(fn, rc)
 
 
 def _x_operands(desc, R, x, x_scales):
     """The backward calls' x: bf16 rows or a checkpoint."""
     if desc.ckpt not in _CODES:
-        return [("x", x, R * desc.in_features, (_BF16,))]
+        return [("x", x, R * desc.in_features, _BF16)]
     codes, scales = _CODES[desc.ckpt]
     return [("x", x, R * desc.in_features, codes),
             ("x_scales", x_scales, R * (desc.in_features // 32), scales)]
-
-
-def _offsets_operand(desc, offsets):
-    return ("expert_offsets", offsets, desc.n_experts + 1, (_I32,))
 
 
 def fw_moe_dense_validate(desc):
@@ -332,87 +345,73 @@ def fw_moe_dense_workspace_size(desc, max_R):
 
 def fw_moe_glu_forward(desc, R, x, w_gate, w_up, expert_offsets, h, workspace, ws_bytes=None,
                        stream=None):
-    xs, ys, ws, _ = _sizes(desc, R)
-    return _launch(
-        "fw_moe_glu_forward",
-        [("x", x, xs, (_BF16,)), ("w_gate", w_gate, ws, (_BF16,)), ("w_up", w_up, ws, (_BF16,)),
-         _offsets_operand(desc, expert_offsets), ("h", h, ys, (_OUT.get(desc.out_dtype),))],
-        workspace, ws_bytes, stream, lambda nb, s: lib().fw_moe_glu_forward(
-            ctypes.byref(desc), R, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(expert_offsets),
-            _ptr(h), _ptr(workspace), nb, s))
+    K, N, E = desc.in_features, desc.out_features, desc.n_experts
+    return _call("fw_moe_glu_forward", desc, R,
+                 (("x", x, R * K, _BF16), ("w_gate", w_gate, E * N * K, _BF16),
+                  ("w_up", w_up, E * N * K, _BF16),
+                  ("expert_offsets", expert_offsets, E + 1, _I32),
+                  ("h", h, R * N, _OUT.get(desc.out_dtype, ()))),
+                 (x, w_gate, w_up, expert_offsets, h), (workspace, True), ws_bytes, stream)
 
 
 def fw_moe_glu_backward(desc, R, x, x_scales, w_gate, w_up, expert_offsets, dh, dx, dw_gate,
                         dw_up, h, workspace, ws_bytes=None, stream=None):
-    xs, ys, ws, _ = _sizes(desc, R)
-    grad = (_OUT.get(desc.grad_dtype),)
-    return _launch(
-        "fw_moe_glu_backward",
-        _x_operands(desc, R, x, x_scales) +
-        [("w_gate", w_gate, ws, (_BF16,)), ("w_up", w_up, ws, (_BF16,)),
-         _offsets_operand(desc, expert_offsets), ("dh", dh, ys, (_BF16,)), ("dx", dx, xs, grad),
-         ("dw_gate", dw_gate, ws, grad), ("dw_up", dw_up, ws, grad), ("h", h, ys, (_BF16,))],
-        workspace, ws_bytes, stream, lambda nb, s: lib().fw_moe_glu_backward(
-            ctypes.byref(desc), R, _ptr(x), _ptr(x_scales), _ptr(w_gate), _ptr(w_up),
-            _ptr(expert_offsets), _ptr(dh), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), _ptr(h),
-            _ptr(workspace), nb, s))
+    K, N, E = desc.in_features, desc.out_features, desc.n_experts
+    grad = _OUT.get(desc.grad_dtype, ())
+    return _call("fw_moe_glu_backward", desc, R,
+                 _x_operands(desc, R, x, x_scales) +
+                 [("w_gate", w_gate, E * N * K, _BF16), ("w_up", w_up, E * N * K, _BF16),
+                  ("expert_offsets", expert_offsets, E + 1, _I32), ("dh", dh, R * N, _BF16),
+                  ("dx", dx, R * K, grad), ("dw_gate", dw_gate, E * N * K, grad),
+                  ("dw_up", dw_up, E * N * K, grad), ("h", h, R * N, _BF16)],
+                 (x, x_scales, w_gate, w_up, expert_offsets, dh, dx, dw_gate, dw_up, h),
+                 (workspace, True), ws_bytes, stream)
 
 
 def fw_moe_linear_forward(desc, R, x, w, bias, residual, expert_offsets, y, workspace,
                           ws_bytes=None, stream=None):
-    xs, ys, ws, bs = _sizes(desc, R)
-    out = (_OUT.get(desc.out_dtype),)
-    return _launch(
-        "fw_moe_linear_forward",
-        [("x", x, xs, (_BF16,)), ("w", w, ws, (_BF16,)), ("bias", bias, bs, (_F32,)),
-         ("residual", residual, ys, out), _offsets_operand(desc, expert_offsets),
-         ("y", y, ys, out)],
-        workspace, ws_bytes, stream, lambda nb, s: lib().fw_moe_linear_forward(
-            ctypes.byref(desc), R, _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
-            _ptr(expert_offsets), _ptr(y), _ptr(workspace), nb, s))
+    K, N, E = desc.in_features, desc.out_features, desc.n_experts
+    out = _OUT.get(desc.out_dtype, ())
+    return _call("fw_moe_linear_forward", desc, R,
+                 (("x", x, R * K, _BF16), ("w", w, E * N * K, _BF16), ("bias", bias, E * N, _F32),
+                  ("residual", residual, R * N, out),
+                  ("expert_offsets", expert_offsets, E + 1, _I32), ("y", y, R * N, out)),
+                 (x, w, bias, residual, expert_offsets, y), (workspace, True), ws_bytes, stream)
 
 
 def fw_moe_linear_backward(desc, R, x, x_scales, w, bias, expert_offsets, dy, dx, dw, dbias,
                            workspace, ws_bytes=None, stream=None):
-    xs, ys, ws, bs = _sizes(desc, R)
-    grad = (_OUT.get(desc.grad_dtype),)
-    return _launch(
-        "fw_moe_linear_backward",
-        _x_operands(desc, R, x, x_scales) +
-        [("w", w, ws, (_BF16,)), ("bias", bias, bs, (_F32,)),
-         _offsets_operand(desc, expert_offsets), ("dy", dy, ys, (_BF16,)), ("dx", dx, xs, grad),
-         ("dw", dw, ws, grad), ("dbias", dbias, bs, (_F32,))],
-        workspace, ws_bytes, stream, lambda nb, s: lib().fw_moe_linear_backward(
-            ctypes.byref(desc), R, _ptr(x), _ptr(x_scales), _ptr(w), _ptr(bias),
-            _ptr(expert_offsets), _ptr(dy), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(workspace), nb,
-            s))
+    K, N, E = desc.in_features, desc.out_features, desc.n_experts
+    grad = _OUT.get(desc.grad_dtype, ())
+    return _call("fw_moe_linear_backward", desc, R,
+                 _x_operands(desc, R, x, x_scales) +
+                 [("w", w, E * N * K, _BF16), ("bias", bias, E * N, _F32),
+                  ("expert_offsets", expert_offsets, E + 1, _I32), ("dy", dy, R * N, _BF16),
+                  ("dx", dx, R * K, grad), ("dw", dw, E * N * K, grad),
+                  ("dbias", dbias, E * N, _F32)],
+                 (x, x_scales, w, bias, expert_offsets, dy, dx, dw, dbias), (workspace, True),
+                 ws_bytes, stream)
 
 
 def _ckpt_operands(desc, R, codes, scales):
     code_types, scale_types = _CODES.get(desc.format, ((), ()))
-    return [("codes", codes, R * desc.features, code_types),
-            ("scales", scales, R * (desc.features // 32), scale_types)]
+    return (("codes", codes, R * desc.features, code_types),
+            ("scales", scales, R * (desc.features // 32), scale_types))
 
 
 def fw_moe_ckpt_pack(desc, R, x, codes, scales, workspace, stream=None):
-    """workspace: a uint8 tensor of at least 256 bytes (its status word)."""
-    if workspace is not None and not isinstance(workspace, int) and \
+    """workspace: a tensor of at least 256 bytes (its status word)."""
+    if workspace is not None and type(workspace) is not int and \
             workspace.numel() * workspace.element_size() < 256:
         raise FwMoeError("fw_moe_ckpt_pack", FW_EWORKSPACE)
-    return _launch(
-        "fw_moe_ckpt_pack",
-        [("x", x, R * desc.features, (_OUT.get(desc.src_dtype),))] +
-        _ckpt_operands(desc, R, codes, scales),
-        workspace, None if not isinstance(workspace, int) else 256, stream,
-        lambda nb, s: lib().fw_moe_ckpt_pack(ctypes.byref(desc), R, _ptr(x), _ptr(codes),
-                                             _ptr(scales), _ptr(workspace), s))
+    return _call("fw_moe_ckpt_pack", desc, R,
+                 (("x", x, R * desc.features, _OUT.get(desc.src_dtype, ())),) +
+                 _ckpt_operands(desc, R, codes, scales),
+                 (x, codes, scales), (workspace, False), None, stream)
 
 
 def fw_moe_ckpt_unpack(desc, R, codes, scales, x, stream=None):
-    return _launch(
-        "fw_moe_ckpt_unpack",
-        _ckpt_operands(desc, R, codes, scales) +
-        [("x", x, R * desc.features, (_OUT.get(desc.dst_dtype),))],
-        None, 0, stream,
-        lambda nb, s: lib().fw_moe_ckpt_unpack(ctypes.byref(desc), R, _ptr(codes), _ptr(scales),
-                                               _ptr(x), s))
+    return _call("fw_moe_ckpt_unpack", desc, R,
+                 _ckpt_operands(desc, R, codes, scales) +
+                 (("x", x, R * desc.features, _OUT.get(desc.dst_dtype, ())),),
+                 (codes, scales, x), None, None, stream)
