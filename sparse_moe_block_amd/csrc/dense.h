@@ -25,6 +25,10 @@ struct DenseWs {
 // serves both.
 DenseWs dense_ws(const fw_moe_dense_desc &d, int R);
 
+// Tile shapes (dense.hip) and their rows.
+enum DenseTile { kTile64, kTile128D, kTile128, kTile256 };
+constexpr int tile_rows(DenseTile t) { return t == kTile256 ? 256 : t == kTile64 ? 64 : 128; }
+
 // One product over row tiles: out rows from rows of q (bf16 [R][Kd], row pitch
 // Kd) times weights, with an epilogue.
 //   kGlu      h = f(q Wg^T) * (q Wu^T)
@@ -47,7 +51,7 @@ struct RowsArgs {
     const int4 *tiles;         // row tiles, or nullptr: all R rows of expert 0
     WsHeader *hdr;
     int max_tiles;
-    int tile_rows;             // 64, 128 or 256 (dense_tile_rows)
+    DenseTile tile;
     const float *bias;         // [E][Np] or nullptr
     const void *residual;      // out's type, or nullptr
     const uint16_t *dy;        // bf16 [R][Np]: the arriving gradient
@@ -57,9 +61,9 @@ struct RowsArgs {
     float *bpart;              // kLinGrad: [row tile][Np] or nullptr
 };
 constexpr int kCus = 256;      // the MI355X's compute units
-// Rows of a row tile: one choice per call when the tiles come from a schedule,
+// The tile shape: one choice per call when the row tiles come from a schedule,
 // per product (`cols` output columns) otherwise.
-int dense_tile_rows(int R, int E, int cols, bool grouped);
+DenseTile dense_tile(int R, int E, int cols, bool grouped);
 hipError_t launch_rows(DenseOp op, const RowsArgs &a, hipStream_t s);
 
 // kGlu and kLinear for few rows an expert (dense_few.hip), straight from

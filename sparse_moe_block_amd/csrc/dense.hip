@@ -62,7 +62,7 @@ __global__ __launch_bounds__(kPrepThreads) void dense_schedule_kernel(
 // so that an XCD's workgroups in flight share few weight and few row panels in
 // its L2.  -1: none.
 constexpr int kBlockRows = 8;
-__device__ __forceinline__ int dense_tile(int row_tiles, int col_tiles, int &ct) {
+__device__ __forceinline__ int dense_block(int row_tiles, int col_tiles, int &ct) {
     const int total = row_tiles * col_tiles, per = (total + 7) / 8;
     const int idx = blockIdx.x / 8, id = (blockIdx.x % 8) * per + idx;
     ct = 0;
@@ -73,35 +73,39 @@ __device__ __forceinline__ int dense_tile(int row_tiles, int col_tiles, int &ct)
     return r0 + in % n;
 }
 
-// Tile shapes by rows (and columns).  256: eight wavefronts of 64 x 128 outputs,
-// one workgroup a CU.  128: four wavefronts of 64 x 64, two workgroups a CU.  64:
-// four wavefronts of 32 x 32 and stages of 128 reduction steps, two workgroups a
-// CU: for products of few tiles, whose time is the number of steps.
-template <int ROWS, bool PX, bool QX, bool DUAL>
+// Tile shapes.
+//  kTile256   256 x 256, eight wavefronts of 64 x 128 outputs, two stages, one
+//             workgroup a CU: the fewest bytes from L2 and LDS an output
+//  kTile128   128 x 128, four wavefronts of 64 x 64, two stages, two workgroups
+//             a CU
+//  kTile128D  128 x 128, eight wavefronts of 32 x 64, four stages, one workgroup
+//             a CU: for products whose tiles do not fill the CUs twice
+//  kTile64    64 x 64, four wavefronts of 32 x 32, four stages, two workgroups a
+//             CU: for products of few tiles
+template <DenseTile TILE, bool PX, bool QX, bool DUAL>
 using TileShape = std::conditional_t<
-    ROWS == 256, Shape<256, 256, 4, 2, 1, PX, QX, DUAL>,
-    std::conditional_t<ROWS == 128, Shape<128, 128, 2, 2, 1, PX, QX, DUAL>,
-                       Shape<64, 64, 2, 2, 2, PX, QX, DUAL>>>;
-template <DenseOp OP, int ROWS>
-using RowShape = TileShape<ROWS, OP == kInput, false, OP == kGlu || OP == kGluGrad>;
-template <int ROWS> constexpr int kThreads = ROWS == 256 ? 512 : 256;
-template <int ROWS> constexpr int kBlocksPerCu = ROWS == 256 ? 1 : 2;
+    TILE == kTile256, Shape<256, 256, 4, 2, 2, PX, QX, DUAL>,
+    std::conditional_t<TILE == kTile128, Shape<128, 128, 2, 2, 2, PX, QX, DUAL>,
+                       std::conditional_t<TILE == kTile128D, Shape<128, 128, 4, 2, 4, PX, QX, DUAL>,
+                                          Shape<64, 64, 2, 2, 4, PX, QX, DUAL>>>>;
+template <DenseOp OP, DenseTile TILE>
+using RowShape = TileShape<TILE, OP == kInput, false, OP == kGlu || OP == kGluGrad>;
+template <DenseTile TILE>
+constexpr int kThreads = TILE == kTile256 || TILE == kTile128D ? 512 : 256;
+template <DenseTile TILE> constexpr int kBlocksPerCu = kThreads<TILE> == 512 ? 1 : 2;
 
 // One (row tile, column tile).
-template <DenseOp OP, int ROWS>
-__global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void rows_kernel(
+template <DenseOp OP, DenseTile TILE>
+__global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void rows_kernel(
     RowsArgs a, int col_tiles, int row_tiles) {
-    using S = RowShape<OP, ROWS>;
-    __shared__ uint4 P0[S::PChunks];
-    __shared__ uint4 P1[S::PChunks];
-    __shared__ uint4 Q0[S::QChunks];
-    __shared__ uint4 Q1[S::QChunks];
+    using S = RowShape<OP, TILE>;
+    FW_RING(S, ring);
     constexpr int BC = S::DUAL ? S::BP / 2 : S::BP;   // output columns of a tile
     int ct, rt;
     if (a.tiles)
         rt = xcd_row_tile(a.hdr, col_tiles, row_tiles, 0, 0, ct);
     else
-        rt = dense_tile(row_tiles, col_tiles, ct);
+        rt = dense_block(row_tiles, col_tiles, ct);
     if (rt < 0) return;
     int expert = 0, rb = rt * S::BQ, rows = min(S::BQ, a.R - rb);
     if (a.tiles) {
@@ -127,7 +131,7 @@ __global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void rows_kerne
         return Operand{(const char *)(a.w1 + we + (size_t)c0 * a.Kd), cols, qpitch, 0};
     };
     f4 acc[S::PI][S::QJ];
-    tile_product<S>(acc, P0, P1, Q0, Q1, wave, lane, a.Kd, a.nseg, p, pb, q);
+    tile_product<S>(acc, ring, wave, lane, a.Kd, a.nseg, p, pb, q);
 
     const size_t dzu = (size_t)a.R * a.Np;   // du behind dg
     float bias[8], colsum[8];
@@ -152,7 +156,7 @@ __global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void rows_kerne
         }
         return e;
     };
-    hand_out<S>(acc, P0, wave, lane, fetch,
+    hand_out<S>(acc, ring.p[0], wave, lane, fetch,
                 [&](int row, int col, float *v, const float *u, const Eight &e) {
         if (!inside(row, col)) return;
         const size_t at = place(row, col);
@@ -204,7 +208,7 @@ __global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void rows_kerne
         // of the column, in a fixed order
         constexpr int CW = kOutCols<S>, LR = CW / 8;
         const int wp = wave % S::WP, wq = wave / S::WP;
-        float *part = (float *)Q0;   // [WQ][BP]
+        float *part = (float *)ring.q[0];   // [WQ][BP]
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             float s = colsum[t];
@@ -223,14 +227,11 @@ __global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void rows_kerne
 }
 
 // dw tiles: Q = output features (rows of dw), P = input features.
-template <int ROWS>
-__global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void grad_kernel(
+template <DenseTile TILE>
+__global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void grad_kernel(
     GradArgs a, int nt, int kt, int tiles) {
-    using S = TileShape<ROWS, true, true, false>;
-    __shared__ uint4 P0[S::PChunks];
-    __shared__ uint4 P1[S::PChunks];
-    __shared__ uint4 Q0[S::QChunks];
-    __shared__ uint4 Q1[S::QChunks];
+    using S = TileShape<TILE, true, true, false>;
+    FW_RING(S, ring);
     // XCD x takes an eighth of the tile list (k tiles fastest)
     const int per = (tiles + 7) / 8;
     const int id = (blockIdx.x % 8) * per + blockIdx.x / 8;
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void grad_kerne
         return Operand{(const char *)x, 0, 2u * (uint32_t)a.K, 2u * (uint32_t)k0};
     };
     f4 acc[S::PI][S::QJ];
-    tile_product<S>(acc, P0, P1, Q0, Q1, wave, lane, e - b, 1, p, p, q);
+    tile_product<S>(acc, ring, wave, lane, e - b, 1, p, p, q);
 
     void *dw = mat ? a.dw1 : a.dw0;
     auto inside = [&](int n, int k) { return n0 + n < a.N && k0 + k < a.K; };
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(kThreads<ROWS>, kBlocksPerCu<ROWS>) void grad_kerne
         if (a.accumulate && inside(n, k)) load8(e, dw, a.out_f32, place(n, k));
         return e;
     };
-    hand_out<S>(acc, P0, wave, lane, fetch,
+    hand_out<S>(acc, ring.p[0], wave, lane, fetch,
                 [&](int n, int k, float *v, const float *, const Eight &e) {
         if (!inside(n, k)) return;
         if (a.accumulate) {
@@ -355,47 +356,47 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float *__restrict_
     db[(size_t)e * N + c] = s + sum;
 }
 
-template <DenseOp OP, int ROWS> hipError_t run_rows(const RowsArgs &a, hipStream_t s) {
-    using S = RowShape<OP, ROWS>;
+template <DenseOp OP, DenseTile TILE> hipError_t run_rows(const RowsArgs &a, hipStream_t s) {
+    using S = RowShape<OP, TILE>;
     constexpr int BC = S::DUAL ? S::BP / 2 : S::BP;
     const int ct = (a.Np + BC - 1) / BC;
     const int rt = a.tiles ? a.max_tiles : (a.R + S::BQ - 1) / S::BQ;
     const int per = a.tiles ? xcd_tile_cap(a.R, a.E, S::BQ, a.max_tiles) * ct : (rt * ct + 7) / 8;
-    rows_kernel<OP, ROWS><<<8 * per, S::Threads, 0, s>>>(a, ct, rt);
+    rows_kernel<OP, TILE><<<8 * per, S::Threads, 0, s>>>(a, ct, rt);
     return hipGetLastError();
 }
 template <DenseOp OP> hipError_t pick_rows(const RowsArgs &a, hipStream_t s) {
-    return a.tile_rows == 256   ? run_rows<OP, 256>(a, s)
-           : a.tile_rows == 128 ? run_rows<OP, 128>(a, s)
-                                : run_rows<OP, 64>(a, s);
+    switch (a.tile) {
+        case kTile256: return run_rows<OP, kTile256>(a, s);
+        case kTile128: return run_rows<OP, kTile128>(a, s);
+        case kTile128D: return run_rows<OP, kTile128D>(a, s);
+        default: return run_rows<OP, kTile64>(a, s);
+    }
 }
 
-template <int ROWS> hipError_t run_grad(const GradArgs &a, hipStream_t s) {
-    const int nt = (a.N + ROWS - 1) / ROWS, kt = (a.K + ROWS - 1) / ROWS;
+template <DenseTile TILE> hipError_t run_grad(const GradArgs &a, hipStream_t s) {
+    constexpr int B = tile_rows(TILE);
+    const int nt = (a.N + B - 1) / B, kt = (a.K + B - 1) / B;
     const int tiles = a.E * a.mats * nt * kt;
-    grad_kernel<ROWS><<<(tiles + 7) / 8 * 8, kThreads<ROWS>, 0, s>>>(a, nt, kt, tiles);
+    grad_kernel<TILE><<<(tiles + 7) / 8 * 8, kThreads<TILE>, 0, s>>>(a, nt, kt, tiles);
     return hipGetLastError();
 }
 
 // The tile shape that takes the least time for `tiles(rows)` tiles, in percent
-// of a round of 256-row tiles.  Measured: 2048 x 4096 -> 1536 in 89 us with 48
-// tiles of 256, 48 us with 192 of 128 (one a CU); 4096 x 7168 -> 2048 in 150 us
-// with 128 tiles of 256, 119 us with 512 of 128 (two a CU); 777 x 4096 -> 1536
-// in 38 us with 84 tiles of 128, 26 us with 312 of 64; 777 x 1536 -> 4096 in 25
-// us with 224 tiles of 128, 28 us with 832 of 64.
-template <class F> int best_tile(F &&tiles) {
+// of a round of 256-row tiles.
+template <class F> DenseTile best_tile(F &&tiles) {
     const int64_t large = tiles(256), small = tiles(128), tiny = tiles(64);
     auto rounds = [](int64_t n, int64_t per) { return (n + per - 1) / per; };
     const int64_t l = rounds(large, kCus) * 100;
-    const int64_t s = small <= kCus ? 45 : rounds(small, 2 * kCus) * 65;
+    const int64_t s = small <= kCus ? 40 : rounds(small, 2 * kCus) * 65;
     const int64_t t = rounds(tiny, 2 * kCus) * 31;
-    return l <= s && l <= t ? 256 : s <= t ? 128 : 64;
+    return l <= s && l <= t ? kTile256 : s <= t ? (small <= kCus ? kTile128D : kTile128) : kTile64;
 }
 
 }  // namespace
 
-int dense_tile_rows(int R, int E, int cols, bool grouped) {
-    if (grouped) return R >= E * 256LL ? 256 : R >= E * 64LL ? 128 : 64;
+DenseTile dense_tile(int R, int E, int cols, bool grouped) {
+    if (grouped) return R >= E * 256LL ? kTile256 : R >= E * 64LL ? kTile128 : kTile64;
     return best_tile([&](int r) { return (int64_t)((R + r - 1) / r) * ((cols + r - 1) / r); });
 }
 
@@ -418,8 +419,12 @@ int64_t grad_tiles(int E, int N, int K, int mats, int rows) {
 }
 
 hipError_t launch_grad(const GradArgs &a, hipStream_t s) {
-    const int rows = best_tile([&](int r) { return grad_tiles(a.E, a.N, a.K, a.mats, r); });
-    return rows == 256 ? run_grad<256>(a, s) : rows == 128 ? run_grad<128>(a, s) : run_grad<64>(a, s);
+    switch (best_tile([&](int r) { return grad_tiles(a.E, a.N, a.K, a.mats, r); })) {
+        case kTile256: return run_grad<kTile256>(a, s);
+        case kTile128: return run_grad<kTile128>(a, s);
+        case kTile128D: return run_grad<kTile128D>(a, s);
+        default: return run_grad<kTile64>(a, s);
+    }
 }
 
 hipError_t launch_colsum(const uint16_t *dy, int R, int N, const int4 *tiles, WsHeader *hdr,

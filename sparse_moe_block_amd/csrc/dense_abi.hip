@@ -96,13 +96,12 @@ struct Call {
           s((hipStream_t)stream) {}
 
     int schedule() const {
-        return offsets ? hip_status(launch_dense_schedule(offsets, d.n_experts, R, tile_rows(0), L, ws, s))
+        return offsets ? hip_status(launch_dense_schedule(offsets, d.n_experts, R,
+                                                          tile_rows(tile(0)), L, ws, s))
                        : FW_OK;
     }
-    // rows of a row tile of a product with cols output columns (both matrices')
-    int tile_rows(int cols) const {
-        return dense_tile_rows(R, d.n_experts, cols, offsets != nullptr);
-    }
+    // the tile shape of a product with cols output columns (both matrices')
+    DenseTile tile(int cols) const { return dense_tile(R, d.n_experts, cols, offsets != nullptr); }
     bool few() const { return few_rows(R, d.n_experts, d.in_features); }
     const int4 *tiles() const { return offsets ? (const int4 *)(ws + L.tiles) : nullptr; }
     // forward-shaped product: x [R][K] times weights [N][K]
@@ -121,7 +120,7 @@ struct Call {
         a.tiles = tiles();
         a.hdr = (WsHeader *)ws;
         a.max_tiles = L.max_tiles;
-        a.tile_rows = tile_rows(w1 ? 2 * a.Np : a.Np);
+        a.tile = tile(w1 ? 2 * a.Np : a.Np);
         return a;
     }
     // dx = dz0 w0 (+ dz1 w1), dz1 behind dz0
@@ -131,7 +130,7 @@ struct Call {
         a.Kd = d.out_features;
         a.nseg = w1 ? 2 : 1;
         a.Np = d.in_features;
-        a.tile_rows = tile_rows(a.Np);
+        a.tile = tile(a.Np);
         a.out = dx;
         a.out_f32 = d.grad_dtype == FW_F32;
         return hip_status(launch_rows(kInput, a, s));
@@ -260,7 +259,7 @@ int fw_moe_linear_backward(const fw_moe_dense_desc *desc, int32_t R, const void 
     const Call c(*desc, R, expert_offsets, workspace, stream);
     const uint16_t *xv = nullptr, *dz = (const uint16_t *)dy;
     float *bpart = (float *)(c.ws + c.L.bpart);
-    const int tile_rows = c.tile_rows(desc->out_features);
+    const int part_rows = tile_rows(c.tile(desc->out_features));
     if (need_x && (rc = c.values(x, x_scales, &xv)) != FW_OK) return rc;
     if (R > 0) {
         if ((rc = c.schedule()) != FW_OK) return rc;
@@ -274,14 +273,14 @@ int fw_moe_linear_backward(const fw_moe_dense_desc *desc, int32_t R, const void 
             if ((rc = hip_status(launch_rows(kLinGrad, a, c.s))) != FW_OK) return rc;
         } else if (dbias) {
             rc = hip_status(launch_colsum(dz, R, desc->out_features, c.tiles(),
-                                          (WsHeader *)c.ws, c.L.max_tiles, tile_rows, bpart, c.s));
+                                          (WsHeader *)c.ws, c.L.max_tiles, part_rows, bpart, c.s));
             if (rc != FW_OK) return rc;
         }
         if (dx && (rc = c.input_grad(dz, w, nullptr, dx)) != FW_OK) return rc;
     }
     if (dbias) {
         rc = hip_status(launch_bias_grad(bpart, expert_offsets, R, desc->n_experts,
-                                         desc->out_features, c.L.max_tiles, tile_rows, dbias,
+                                         desc->out_features, c.L.max_tiles, part_rows, dbias,
                                          desc->accumulate, c.s));
         if (rc != FW_OK) return rc;
     }

@@ -1,7 +1,7 @@
 // The bf16 MFMA tile product of the training kernels: one workgroup forms a
 // BP x BQ tile of P Q^T over a reduction of any length, operands staged HBM/L2
-// -> LDS by range-checked DMA, 64 reduction steps at a time, into one of two
-// buffers while the other is used.
+// -> LDS by range-checked DMA, 64 reduction steps a stage, in a ring of two to
+// four stages.
 //
 // Each operand is either stored along the reduction (its rows are the tile's
 // rows, "along") or across it (its rows are reduction steps, "across": weight
@@ -32,15 +32,15 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
-constexpr int kStepK = 64;                  // reduction steps per block of a stage
+constexpr int kStepK = 64;                  // reduction steps per stage
 constexpr int kSlices = kStepK / 32;        // of 32, one MFMA deep
 constexpr uint32_t kNoChunk = 0x80000000u;  // an offset beyond every range
 
-// BP x BQ tile by WP x WQ wavefronts, D blocks of 64 steps a stage; PX / QX: the
-// operand is stored across.
-template <int BP_, int BQ_, int WP_, int WQ_, int D_, bool PX_, bool QX_, bool DUAL_>
+// BP x BQ tile by WP x WQ wavefronts, NS stages of 64 reduction steps; PX / QX:
+// the operand is stored across.
+template <int BP_, int BQ_, int WP_, int WQ_, int NS_, bool PX_, bool QX_, bool DUAL_>
 struct Shape {
-    static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, D = D_;
+    static constexpr int BP = BP_, BQ = BQ_, WP = WP_, WQ = WQ_, NS = NS_;
     static constexpr bool PX = PX_, QX = QX_;
     // the P tile is half of one matrix and half of another, so that a wavefront
     // holds the same columns of both
@@ -48,10 +48,9 @@ struct Shape {
     static constexpr int NW = WP * WQ, Threads = 64 * NW;
     static constexpr int PI = BP / WP / 16, QJ = BQ / WQ / 16;
     // 16-byte chunks of a stage
-    static constexpr int PChunks = D * BP * kStepK / 8, QChunks = D * BQ * kStepK / 8;
+    static constexpr int PChunks = BP * kStepK / 8, QChunks = BQ * kStepK / 8;
     static_assert(!DUAL || PI % 2 == 0, "a dual tile's wavefront holds as many groups of each matrix");
-    static_assert(PChunks % (D * Threads) == 0 && QChunks % (D * Threads) == 0,
-                  "whole DMA instructions");
+    static_assert(PChunks % Threads == 0 && QChunks % Threads == 0, "whole DMA instructions");
     // tile index of the first row of wavefront wp's P group i
     static __device__ __forceinline__ int prow(int wp, int i) {
         return DUAL ? i / (PI / 2) * (BP / 2) + wp * (BP / 2 / WP) + 16 * (i % (PI / 2))
@@ -160,13 +159,33 @@ template <int ROWS, bool ACROSS, int N> struct Reader {
     }
 };
 
+// The stages' LDS: arrays of their own, so that the compiler knows that a
+// pending DMA and a read touch different ones.
+template <class S> struct Ring {
+    uint4 *p[S::NS], *q[S::NS];
+};
+#define FW_STAGE(S, n)                                          \
+    __shared__ uint4 fw_p##n[S::NS > n ? S::PChunks : 1];       \
+    __shared__ uint4 fw_q##n[S::NS > n ? S::QChunks : 1];       \
+    if constexpr (S::NS > n) {                                  \
+        fw_ring.p[n] = fw_p##n;                                 \
+        fw_ring.q[n] = fw_q##n;                                 \
+    }
+#define FW_RING(S, name) \
+    Ring<S> fw_ring;     \
+    FW_STAGE(S, 0)       \
+    FW_STAGE(S, 1)       \
+    FW_STAGE(S, 2)       \
+    FW_STAGE(S, 3)       \
+    const Ring<S> &name = fw_ring
+
 // acc[i][j] (PI x QJ groups of 16 x 16) = the tile product over nseg segments
 // of Kd steps; p(seg) / pb(seg) and q(seg) give the operands (pb: the second
 // matrix of a dual P tile).
 template <class S, class PF, class PBF, class QF>
-__device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], uint4 *P0, uint4 *P1,
-                                             uint4 *Q0, uint4 *Q1, int wave, int lane, int Kd,
-                                             int nseg, PF &&p, PBF &&pb, QF &&q) {
+__device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], const Ring<S> &ring,
+                                             int wave, int lane, int Kd, int nseg, PF &&p,
+                                             PBF &&pb, QF &&q) {
     const int wp = wave % S::WP, wq = wave / S::WP;
     Stager<S::BP, S::PX, S::NW, S::DUAL> ps;
     Stager<S::BQ, S::QX, S::NW> qs;
@@ -183,41 +202,60 @@ __device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], uint4 *P0,
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.f;
 
-    constexpr int kStage = S::D * kStepK;
-    const int per = (Kd + kStage - 1) / kStage, steps = per * nseg;
+    const int per = (Kd + kStepK - 1) / kStepK, steps = per * nseg;
     if (steps == 0) return;
     // The addresses of step st's stage.  `whole`: all of its 64 reduction steps
     // are there, which lets the DMA do without the test of each chunk; otherwise
     // chunks outside (and past the last step everything) read as zeros.
     struct Next {
-        rsrc_t q[S::D], p[S::D], pb[S::DUAL ? S::D : 1];
+        rsrc_t q, p, pb;
         int k, kd;
     };
     auto prepare = [&](int st) {
-        Next n;
-        const int seg = st >= per;   // nseg <= 2
-        n.k = (st - seg * per) * kStage;
-        n.kd = st < steps ? Kd : 0;
-#pragma unroll
-        for (int d = 0; d < S::D; ++d) {
-            n.q[d] = qs.rsrc(q(seg), n.k + d * kStepK, n.kd);
-            n.p[d] = ps.rsrc(p(seg), n.k + d * kStepK, n.kd);
-            if constexpr (S::DUAL) n.pb[d] = ps.rsrc(pb(seg), n.k + d * kStepK, n.kd);
-        }
+        const int seg = st >= per, k = (st - seg * per) * kStepK;   // nseg <= 2
+        const int kd = st < steps ? Kd : 0;
+        return Next{qs.rsrc(q(seg), k, kd), ps.rsrc(p(seg), k, kd),
+                    S::DUAL ? ps.rsrc(pb(seg), k, kd) : ps.rsrc(p(seg), k, kd), k, kd};
+    };
+    // The same for whole stages, one after the other from `at` on: a few scalar
+    // additions (the general form's fifty scalar instructions took a tenth of a
+    // large tile's step and a quarter of a small one's).
+    struct {
+        const char *q, *p, *pb;
+        int qn, pn;   // range lengths
+    } at;
+    auto start = [&](int seg, int k) {
+        const Operand oq = q(seg), op = p(seg);
+        const int64_t qk = S::QX ? (int64_t)k * oq.pitch : 2 * (int64_t)k;
+        const int64_t pk = S::PX ? (int64_t)k * op.pitch : 2 * (int64_t)k;
+        at.q = oq.base + qk;
+        at.p = op.base + pk;
+        at.pb = S::DUAL ? pb(seg).base + pk : nullptr;
+        at.qn = S::QX ? kStepK * (int)oq.pitch - (int)oq.tail : oq.rows * (int)oq.pitch - 2 * k;
+        at.pn = S::PX ? kStepK * (int)op.pitch - (int)op.tail : op.rows * (int)op.pitch - 2 * k;
+    };
+    const int64_t qstep = S::QX ? kStepK * (int64_t)q(0).pitch : 2 * kStepK;
+    const int64_t pstep = S::PX ? kStepK * (int64_t)p(0).pitch : 2 * kStepK;
+    auto advance = [&]() {
+        const Next n{make_rsrc(at.q, at.qn), make_rsrc(at.p, at.pn),
+                     make_rsrc(S::DUAL ? at.pb : at.p, at.pn), 0, 0};
+        at.q += qstep;
+        at.p += pstep;
+        if (S::DUAL) at.pb += pstep;
+        if (!S::QX) at.qn -= 2 * kStepK;
+        if (!S::PX) at.pn -= 2 * kStepK;
         return n;
     };
-    // DMA instruction i of a stage: per block Q's, then P's
-    constexpr int kBlockDma = ps.kInstr + qs.kInstr, kDma = S::D * kBlockDma;
-    auto issue = [&](const Next &n, uint4 *pl, uint4 *ql, int i, auto whole) {
+    // DMA instruction i of a stage (buffer x): Q's, then P's
+    constexpr int kDma = ps.kInstr + qs.kInstr;
+    auto issue = [&](const Next &n, int x, int i, auto whole) {
         constexpr bool W = decltype(whole)::value;
-        if (i >= kDma) return;
-        const int d = i / kBlockDma, j = i % kBlockDma, k = n.k + d * kStepK;
-        if (j < qs.kInstr) {
-            qs.template issue<W>(n.q[d], ql + d * (S::QChunks / S::D), wave, k, n.kd, j);
-        } else {
-            const int m = j - qs.kInstr;
-            ps.template issue<W>(S::DUAL && 2 * m >= ps.kInstr ? n.pb[S::DUAL ? d : 0] : n.p[d],
-                                 pl + d * (S::PChunks / S::D), wave, k, n.kd, m);
+        if (i < qs.kInstr) {
+            qs.template issue<W>(n.q, ring.q[x], wave, n.k, n.kd, i);
+        } else if (i < kDma) {
+            const int j = i - qs.kInstr;
+            ps.template issue<W>(S::DUAL && 2 * j >= ps.kInstr ? n.pb : n.p, ring.p[x], wave, n.k,
+                                 n.kd, j);
         }
     };
     // The slice's operands.  P's are held twice, the next slice's read during
@@ -230,74 +268,85 @@ __device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], uint4 *P0,
         for (int i = 0; i < S::PI; ++i)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s][i], b[j], acc[i][j], 0, 0, 0);
     };
-    // everything issued so far has landed and every wavefront is here
+    // the next step's stage has landed (those behind it may be in flight) and
+    // every wavefront is here
+    constexpr int kBehind = (S::NS - 2) * kDma;
+    static_assert(kBehind < 64, "vmcnt");
     auto sync = [&]() {
-        __builtin_amdgcn_s_waitcnt(7 << 4);   // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt(7 << 4 | kBehind % 16 | kBehind / 16 << 14);   // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
-    // One step: the stage's 32-step slices.  The rendezvous comes behind the last
-    // slice's first group, when all of this buffer is in registers and its MFMAs
-    // cover the wait: from there on the reads are of the next buffer (pn, qn)
-    // and this one is refilled with step st + 2's stage, a few DMA instructions
-    // behind each group (a burst of them would fill the memory pipeline's queue
-    // and hold up the MFMAs behind it).
-    constexpr int kAll = S::D * kSlices;
-    auto slice = [&](int x, const uint4 *pl, const uint4 *ql, int s, auto &&behind) {
-        // reads slice s of (pl, ql) while the present one's MFMAs run
-        const uint4 *pd = pl + s / kSlices * (S::PChunks / S::D);
-        const uint4 *qd = ql + s / kSlices * (S::QChunks / S::D);
+    // The MFMAs of the present slice (P operands a[x]), behind each group the
+    // reads of slice s of buffer `from`.
+    auto slice = [&](int x, int from, int s, auto &&behind) {
 #pragma unroll
         for (int j = 0; j < S::QJ; ++j) {
             group(x, j);
             behind(j);
-            b[j] = qr.read(qd, j, s % kSlices);
-            if (j < S::PI) a[x ^ 1][j] = pr.read(pd, j, s % kSlices);
+            b[j] = qr.read(ring.q[from], j, s);
+            if (j < S::PI) a[x ^ 1][j] = pr.read(ring.p[from], j, s);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    auto step = [&](int st, uint4 *pl, uint4 *ql, const uint4 *pn, const uint4 *qn, auto whole) {
-#pragma unroll
-        for (int s = 0; s + 1 < kAll; ++s) slice(s & 1, pl, ql, s + 1, [](int) {});
-        const Next n = prepare(st + 2);
+    // One step (buffer x): two 32-step slices.  The rendezvous comes behind the
+    // second slice's first group, when all of this buffer is in registers and its
+    // MFMAs cover the wait: from there on the reads are of the next buffer and
+    // this one is refilled with step st + NS's stage, a few DMA instructions
+    // behind each group (a burst of them would fill the memory pipeline's queue
+    // and hold up the MFMAs behind it).
+    static_assert(kSlices == 2, "a step's slices alternate the P operands");
+    auto step = [&](int st, int x, auto whole) {
+        slice(0, x, 1, [](int) {});
+        const Next n = decltype(whole)::value ? advance() : prepare(st + S::NS);
         constexpr int kPer = (kDma + S::QJ - 1) / S::QJ;
-        slice((kAll - 1) & 1, pn, qn, 0, [&](int j) {
+        slice(1, (x + 1) % S::NS, 0, [&](int j) {
             if (j == 0) sync();
 #pragma unroll
-            for (int d = 0; d < kPer; ++d) issue(n, pl, ql, j * kPer + d, whole);
+            for (int d = 0; d < kPer; ++d) issue(n, x, j * kPer + d, whole);
         });
     };
     constexpr auto whole = std::true_type{};
     constexpr auto partial = std::false_type{};
-    Next n = prepare(0);
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) issue(n, P0, Q0, i, partial);
-    n = prepare(1);
+    for (int x = 0; x < S::NS; ++x) {
+        const Next n = prepare(x);
 #pragma unroll
-    for (int i = 0; i < kDma; ++i) issue(n, P1, Q1, i, partial);
-    __builtin_amdgcn_s_waitcnt(7 << 4 | kDma % 16 | kDma / 16 << 14);   // the first stage
+        for (int i = 0; i < kDma; ++i) issue(n, x, i, partial);
+    }
+    constexpr int kFirst = (S::NS - 1) * kDma;   // all but the first stage
+    static_assert(kFirst < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt(7 << 4 | kFirst % 16 | kFirst / 16 << 14);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < S::PI; ++i) a[0][i] = pr.read(P0, i, 0);
+    for (int i = 0; i < S::PI; ++i) a[0][i] = pr.read(ring.p[0], i, 0);
 #pragma unroll
-    for (int j = 0; j < S::QJ; ++j) b[j] = qr.read(Q0, j, 0);
-    // Two steps per turn, so that each buffer keeps its name (the compiler then
-    // knows that a pending DMA and a read touch different arrays).  The first
-    // loop's DMA is of whole stages only (step st issues stage st + 2).
+    for (int j = 0; j < S::QJ; ++j) b[j] = qr.read(ring.q[0], j, 0);
+    // NS steps per turn, so that each buffer keeps its name; step st issues stage
+    // st + NS.  Per segment: turns that issue whole stages of it only, then turns
+    // of any stages up to where the next segment's begin (the end).
     int st = 0;
-    const int full = nseg == 1 || Kd % kStage == 0 ? nseg * (Kd / kStage) : 0;
-    for (; st + 3 < full; st += 2) {
-        step(st, P0, Q0, P1, Q1, whole);
-        step(st + 1, P1, Q1, P0, Q0, whole);
+    for (int seg = 0; seg < nseg; ++seg) {
+        const int first = seg * per, full = first + Kd / kStepK;
+        start(seg, (st + S::NS - first) * kStepK);
+        for (; st + 2 * S::NS <= full; st += S::NS) {
+#pragma unroll
+            for (int x = 0; x < S::NS; ++x) step(st + x, x, whole);
+        }
+        const int until = seg + 1 < nseg ? first + per - S::NS : steps - S::NS + 1;
+        for (; st < until; st += S::NS) {
+#pragma unroll
+            for (int x = 0; x < S::NS; ++x) step(st + x, x, partial);
+        }
     }
-    for (; st + 1 < steps; st += 2) {
-        step(st, P0, Q0, P1, Q1, partial);
-        step(st + 1, P1, Q1, P0, Q0, partial);
-    }
-    if (st < steps) step(st, P0, Q0, P1, Q1, partial);
+#pragma unroll
+    for (int x = 0; x + 1 < S::NS; ++x)
+        if (st + x < steps) step(st + x, x, partial);
     // the last DMA has landed in every wavefront: the buffers are free
-    sync();
+    __builtin_amdgcn_s_waitcnt(7 << 4);   // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Hands the accumulators out by rows: emit(row, col, v, u, e) gets eight
