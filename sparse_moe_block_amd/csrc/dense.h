@@ -26,7 +26,7 @@ struct DenseWs {
 DenseWs dense_ws(const fw_moe_dense_desc &d, int R);
 
 // Tile shapes (dense.hip) and their rows.
-enum DenseTile { kTile64, kTile128D, kTile128, kTile256 };
+enum DenseTile { kTile64, kTile128D, kTile128, kTileWide, kTile256 };
 constexpr int tile_rows(DenseTile t) { return t == kTile256 ? 256 : t == kTile64 ? 64 : 128; }
 
 // One product over row tiles: out rows from rows of q (bf16 [R][Kd], row pitch
@@ -95,9 +95,16 @@ int64_t rows_tiles(int R, int E, int Np);
 // dy; kLinGrad writes the same partials itself), then over e's tiles in order.
 hipError_t launch_colsum(const uint16_t *dy, int R, int N, const int4 *tiles, WsHeader *hdr,
                          int max_tiles, int tile_rows, float *bpart, hipStream_t s);
-hipError_t launch_bias_grad(const float *bpart, const int32_t *offsets, int R, int E, int N,
-                            int max_tiles, int tile_rows, float *db, int accumulate,
-                            hipStream_t s);
+struct BiasArgs {
+    const float *part;         // [row tile][N]
+    const int32_t *offsets;    // as in GradArgs
+    int R, N, max_tiles, tile_rows;
+    float *db;                 // [E][N] (launch_pair: nullptr if not wanted)
+    int accumulate;
+};
+hipError_t launch_bias_grad(const BiasArgs &b, int E, hipStream_t s);
+// dx (kInput), dw and db of one matrix without offsets in one launch.
+hipError_t launch_pair(const RowsArgs &a, const GradArgs &g, const BiasArgs &b, hipStream_t s);
 
 hipError_t launch_dense_schedule(const int32_t *offsets, int E, int R, int tile_rows,
                                  const DenseWs &L, char *ws, hipStream_t s);

@@ -11,6 +11,7 @@
 // bf16 products that follow; the bias gradient is summed before that rounding.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "dense_core.h"
@@ -62,9 +63,9 @@ __global__ __launch_bounds__(kPrepThreads) void dense_schedule_kernel(
 // so that an XCD's workgroups in flight share few weight and few row panels in
 // its L2.  -1: none.
 constexpr int kBlockRows = 8;
-__device__ __forceinline__ int dense_block(int row_tiles, int col_tiles, int &ct) {
+__device__ __forceinline__ int dense_block(int block_id, int row_tiles, int col_tiles, int &ct) {
     const int total = row_tiles * col_tiles, per = (total + 7) / 8;
-    const int idx = blockIdx.x / 8, id = (blockIdx.x % 8) * per + idx;
+    const int idx = block_id / 8, id = (block_id % 8) * per + idx;
     ct = 0;
     if (idx >= per || id >= total) return -1;
     const int block = id / (kBlockRows * col_tiles), in = id % (kBlockRows * col_tiles);
@@ -76,6 +77,8 @@ __device__ __forceinline__ int dense_block(int row_tiles, int col_tiles, int &ct
 // Tile shapes.
 //  kTile256   256 x 256, eight wavefronts of 64 x 128 outputs, two stages, one
 //             workgroup a CU: the fewest bytes from L2 and LDS an output
+//  kTileWide  256 columns x 128 rows, eight wavefronts of 64 x 64, three stages,
+//             one workgroup a CU (row products only)
 //  kTile128   128 x 128, four wavefronts of 64 x 64, two stages, two workgroups
 //             a CU
 //  kTile128D  128 x 128, eight wavefronts of 32 x 64, four stages, one workgroup
@@ -85,28 +88,23 @@ __device__ __forceinline__ int dense_block(int row_tiles, int col_tiles, int &ct
 template <DenseTile TILE, bool PX, bool QX, bool DUAL>
 using TileShape = std::conditional_t<
     TILE == kTile256, Shape<256, 256, 4, 2, 2, PX, QX, DUAL>,
-    std::conditional_t<TILE == kTile128, Shape<128, 128, 2, 2, 2, PX, QX, DUAL>,
-                       std::conditional_t<TILE == kTile128D, Shape<128, 128, 4, 2, 4, PX, QX, DUAL>,
-                                          Shape<64, 64, 2, 2, 4, PX, QX, DUAL>>>>;
+    std::conditional_t<
+        TILE == kTileWide, Shape<256, 128, 4, 2, 3, PX, QX, DUAL>,
+        std::conditional_t<TILE == kTile128, Shape<128, 128, 2, 2, 2, PX, QX, DUAL>,
+                           std::conditional_t<TILE == kTile128D,
+                                              Shape<128, 128, 4, 2, 4, PX, QX, DUAL>,
+                                              Shape<64, 64, 2, 2, 4, PX, QX, DUAL>>>>>;
 template <DenseOp OP, DenseTile TILE>
 using RowShape = TileShape<TILE, OP == kInput, false, OP == kGlu || OP == kGluGrad>;
 template <DenseTile TILE>
-constexpr int kThreads = TILE == kTile256 || TILE == kTile128D ? 512 : 256;
+constexpr int kThreads = TILE == kTile128 || TILE == kTile64 ? 256 : 512;
 template <DenseTile TILE> constexpr int kBlocksPerCu = kThreads<TILE> == 512 ? 1 : 2;
 
-// One (row tile, column tile).
-template <DenseOp OP, DenseTile TILE>
-__global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void rows_kernel(
-    RowsArgs a, int col_tiles, int row_tiles) {
-    using S = RowShape<OP, TILE>;
-    FW_RING(S, ring);
+// One (row tile rt, column tile ct).
+template <DenseOp OP, class S>
+__device__ __forceinline__ void rows_tile(const RowsArgs &a, const Ring<S::NS> &ring, int rt,
+                                          int ct) {
     constexpr int BC = S::DUAL ? S::BP / 2 : S::BP;   // output columns of a tile
-    int ct, rt;
-    if (a.tiles)
-        rt = xcd_row_tile(a.hdr, col_tiles, row_tiles, 0, 0, ct);
-    else
-        rt = dense_block(row_tiles, col_tiles, ct);
-    if (rt < 0) return;
     int expert = 0, rb = rt * S::BQ, rows = min(S::BQ, a.R - rb);
     if (a.tiles) {
         const int4 tl = ld_const(a.tiles + rt);
@@ -226,16 +224,30 @@ __global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void rows_kerne
     }
 }
 
-// dw tiles: Q = output features (rows of dw), P = input features.
-template <DenseTile TILE>
-__global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void grad_kernel(
-    GradArgs a, int nt, int kt, int tiles) {
-    using S = TileShape<TILE, true, true, false>;
+template <DenseOp OP, DenseTile TILE>
+__global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void rows_kernel(
+    RowsArgs a, int col_tiles, int row_tiles) {
+    using S = RowShape<OP, TILE>;
     FW_RING(S, ring);
-    // XCD x takes an eighth of the tile list (k tiles fastest)
-    const int per = (tiles + 7) / 8;
-    const int id = (blockIdx.x % 8) * per + blockIdx.x / 8;
-    if (id >= tiles || (int)(blockIdx.x / 8) >= per) return;
+    int ct, rt;
+    if (a.tiles)
+        rt = xcd_row_tile(a.hdr, col_tiles, row_tiles, 0, 0, ct);
+    else
+        rt = dense_block(blockIdx.x, row_tiles, col_tiles, ct);
+    if (rt >= 0) rows_tile<OP, S>(a, ring, rt, ct);
+}
+
+// XCD x takes an eighth of a list of `tiles`; -1: none.
+__device__ __forceinline__ int grad_block(int block, int tiles) {
+    const int per = (tiles + 7) / 8, id = (block % 8) * per + block / 8;
+    return block / 8 < per && id < tiles ? id : -1;
+}
+
+// dw tile id (k tiles fastest): Q = output features (rows of dw), P = input
+// features.
+template <class S>
+__device__ __forceinline__ void grad_tile(const GradArgs &a, const Ring<S::NS> &ring, int nt,
+                                          int kt, int id) {
     const int k0 = id % kt * S::BP, n_all = id / kt;
     const int n0 = n_all % nt * S::BQ, em = n_all / nt;
     const int mat = em % a.mats, expert = em / a.mats;
@@ -275,6 +287,15 @@ __global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void grad_kerne
         }
         store8(dw, a.out_f32, place(n, k), v);
     });
+}
+
+template <DenseTile TILE>
+__global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void grad_kernel(
+    GradArgs a, int nt, int kt, int tiles) {
+    using S = TileShape<TILE, true, true, false>;
+    FW_RING(S, ring);
+    const int id = grad_block(blockIdx.x, tiles);
+    if (id >= 0) grad_tile<S>(a, ring, nt, kt, id);
 }
 
 // Column sums of one row tile of bf16 rows: a workgroup takes 64 columns,
@@ -320,21 +341,28 @@ __global__ __launch_bounds__(256) void colsum_kernel(const uint16_t *__restrict_
     }
 }
 
-// db[e] = the sum of e's row tiles' partials, in tile order (the schedule
-// lists each expert's tiles in row order, experts ascending).
-__global__ __launch_bounds__(256) void bias_grad_kernel(const float *__restrict__ bpart,
-                                                        const int32_t *__restrict__ offsets,
-                                                        int R, int N, int max_tiles,
-                                                        int tile_rows, float *__restrict__ db,
-                                                        int accumulate) {
+// db[e][c] = the sum of n row tiles' partials from tile `first` on, in order.
+__device__ __forceinline__ void bias_column(const BiasArgs &b, int e, int c, int first, int n) {
+    if (c >= b.N) return;
+    const float s = b.accumulate ? b.db[(size_t)e * b.N + c] : 0.f;
+    const float *p = b.part + (size_t)first * b.N + c;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) sum += p[(size_t)i * b.N];
+    b.db[(size_t)e * b.N + c] = s + sum;
+}
+
+// Expert e's tiles: the schedule lists each expert's in row order, experts
+// ascending.
+__global__ __launch_bounds__(256) void bias_grad_kernel(BiasArgs b) {
     __shared__ int before[256], own;
-    const int e = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
-    int first = 0, n = (R + tile_rows - 1) / tile_rows;
-    if (offsets) {
+    const int e = blockIdx.y;
+    int first = 0, n = (b.R + b.tile_rows - 1) / b.tile_rows;
+    if (b.offsets) {
         int mine = 0;
         for (int i = threadIdx.x; i <= e; i += 256) {
-            const int b = min(max(offsets[i], 0), R), t = min(max(offsets[i + 1], b), R);
-            const int nt = (t - b + tile_rows - 1) / tile_rows;
+            const int r = min(max(b.offsets[i], 0), b.R), t = min(max(b.offsets[i + 1], r), b.R);
+            const int nt = (t - r + b.tile_rows - 1) / b.tile_rows;
             if (i == e) own = nt;
             else mine += nt;
         }
@@ -344,16 +372,42 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const float *__restrict_
             if ((int)threadIdx.x < o) before[threadIdx.x] += before[threadIdx.x + o];
             __syncthreads();
         }
-        first = min(before[0], max_tiles);
-        n = min(own, max_tiles - first);
+        first = min(before[0], b.max_tiles);
+        n = min(own, b.max_tiles - first);
     }
-    if (c >= N) return;
-    const float s = accumulate ? db[(size_t)e * N + c] : 0.f;
-    const float *p = bpart + (size_t)first * N + c;
-    float sum = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) sum += p[(size_t)i * N];
-    db[(size_t)e * N + c] = s + sum;
+    bias_column(b, e, blockIdx.x * 256 + threadIdx.x, first, n);
+}
+
+// dx, dw and the bias gradient of one matrix in one launch: they depend on dz
+// alone, and the tiles of one fill the CUs that the other's leave idle.  Blocks:
+// the product with the longer reduction, the other one, the bias columns.
+// Measured, all three together against launches of their own: 777 rows, 1536 ->
+// 4096: 51 us against 63; 1023 rows, 2048 -> 2 x 1376: 59 us against 63 (whole calls).
+template <DenseTile TILE>
+__global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void pair_kernel(
+    RowsArgs a, GradArgs g, BiasArgs b, int ct_n, int rt_n, int nt, int kt, int dx_blocks,
+    int dw_blocks, int dw_first) {
+    using SR = RowShape<kInput, TILE>;
+    using SG = TileShape<TILE, true, true, false>;
+    static_assert(SR::PChunks == SG::PChunks && SR::QChunks == SG::QChunks, "one ring for both");
+    FW_RING(SR, ring);
+    int i = blockIdx.x;
+    const bool first = i < (dw_first ? dw_blocks : dx_blocks);
+    if (!first) i -= dw_first ? dw_blocks : dx_blocks;
+    if (i >= (dw_first ? dx_blocks : dw_blocks) && !first) {
+        i -= dw_first ? dx_blocks : dw_blocks;
+        bias_column(b, 0, i * kThreads<TILE> + threadIdx.x, 0,
+                    (b.R + b.tile_rows - 1) / b.tile_rows);
+        return;
+    }
+    if (first == (dw_first != 0)) {
+        const int id = grad_block(i, g.mats * nt * kt);
+        if (id >= 0) grad_tile<SG>(g, ring, nt, kt, id);
+    } else {
+        int ct;
+        const int rt = dense_block(i, rt_n, ct_n, ct);
+        if (rt >= 0) rows_tile<kInput, SR>(a, ring, rt, ct);
+    }
 }
 
 template <DenseOp OP, DenseTile TILE> hipError_t run_rows(const RowsArgs &a, hipStream_t s) {
@@ -368,10 +422,23 @@ template <DenseOp OP, DenseTile TILE> hipError_t run_rows(const RowsArgs &a, hip
 template <DenseOp OP> hipError_t pick_rows(const RowsArgs &a, hipStream_t s) {
     switch (a.tile) {
         case kTile256: return run_rows<OP, kTile256>(a, s);
-        case kTile128: return run_rows<OP, kTile128>(a, s);
+        case kTileWide: return run_rows<OP, kTileWide>(a, s);
         case kTile128D: return run_rows<OP, kTile128D>(a, s);
         default: return run_rows<OP, kTile64>(a, s);
     }
+}
+
+template <DenseTile TILE>
+hipError_t run_pair(const RowsArgs &a, const GradArgs &g, const BiasArgs &b, hipStream_t s) {
+    using SR = RowShape<kInput, TILE>;
+    using SG = TileShape<TILE, true, true, false>;
+    const int ct = (a.Np + SR::BP - 1) / SR::BP, rt = (a.R + SR::BQ - 1) / SR::BQ;
+    const int nt = (g.N + SG::BQ - 1) / SG::BQ, kt = (g.K + SG::BP - 1) / SG::BP;
+    const int dx = (rt * ct + 7) / 8 * 8, dw = (g.mats * nt * kt + 7) / 8 * 8;
+    const int db = b.db ? (b.N + kThreads<TILE> - 1) / kThreads<TILE> : 0;
+    pair_kernel<TILE><<<dx + dw + db, kThreads<TILE>, 0, s>>>(
+        a, g, b, ct, rt, nt, kt, dx, dw, g.R > a.nseg * a.Kd);
+    return hipGetLastError();
 }
 
 template <DenseTile TILE> hipError_t run_grad(const GradArgs &a, hipStream_t s) {
@@ -382,22 +449,27 @@ template <DenseTile TILE> hipError_t run_grad(const GradArgs &a, hipStream_t s) 
     return hipGetLastError();
 }
 
-// The tile shape that takes the least time for `tiles(rows)` tiles, in percent
-// of a round of 256-row tiles.
-template <class F> DenseTile best_tile(F &&tiles) {
-    const int64_t large = tiles(256), small = tiles(128), tiny = tiles(64);
-    auto rounds = [](int64_t n, int64_t per) { return (n + per - 1) / per; };
-    const int64_t l = rounds(large, kCus) * 100;
-    const int64_t s = small <= kCus ? 40 : rounds(small, 2 * kCus) * 65;
-    const int64_t t = rounds(tiny, 2 * kCus) * 31;
-    return l <= s && l <= t ? kTile256 : s <= t ? (small <= kCus ? kTile128D : kTile128) : kTile64;
-}
+int64_t rounds(int64_t tiles, int64_t per) { return (tiles + per - 1) / per; }
 
 }  // namespace
 
+// The shape that takes the least time, in percent of a round of 256-row tiles.
+// Measured: 2048 x 4096 -> 1536 in 76 us with 48 tiles of 256, 44 us with 192 of
+// 128 two to a CU, 30 us one to a CU; 4096 x 7168 -> 2048 in 136 us with 128
+// tiles of 256, 105 us with 512 of 128, 95 us with 256 wide ones; 777 x 4096 ->
+// 1536 in 27.4 us with 84 tiles of 128, 25.6 us with 312 of 64; 777 x 1536 ->
+// 4096 in 16.1 us with 224 tiles of 128, 22.7 us with 832 of 64.  Rows in groups
+// of about 128 (2048 -> 2 x 768, 128 groups): 254 us with wide tiles, 265 us with
+// 128 x 128.
 DenseTile dense_tile(int R, int E, int cols, bool grouped) {
-    if (grouped) return R >= E * 256LL ? kTile256 : R >= E * 64LL ? kTile128 : kTile64;
-    return best_tile([&](int r) { return (int64_t)((R + r - 1) / r) * ((cols + r - 1) / r); });
+    if (grouped) return R >= E * 256LL ? kTile256 : R >= E * 64LL ? kTileWide : kTile64;
+    auto tiles = [&](int r, int c) { return (int64_t)((R + r - 1) / r) * ((cols + c - 1) / c); };
+    const int64_t l = rounds(tiles(256, 256), kCus) * 100;
+    const int64_t m = tiles(128, 128) <= kCus ? 40 : rounds(tiles(128, 256), kCus) * 60;
+    const int64_t t = rounds(tiles(64, 64), 2 * kCus) * 31;
+    return l <= m && l <= t ? kTile256
+           : m <= t         ? (tiles(128, 128) <= kCus ? kTile128D : kTileWide)
+                            : kTile64;
 }
 
 hipError_t launch_rows(DenseOp op, const RowsArgs &a, hipStream_t s) {
@@ -419,12 +491,39 @@ int64_t grad_tiles(int E, int N, int K, int mats, int rows) {
 }
 
 hipError_t launch_grad(const GradArgs &a, hipStream_t s) {
-    switch (best_tile([&](int r) { return grad_tiles(a.E, a.N, a.K, a.mats, r); })) {
-        case kTile256: return run_grad<kTile256>(a, s);
-        case kTile128: return run_grad<kTile128>(a, s);
-        case kTile128D: return run_grad<kTile128D>(a, s);
-        default: return run_grad<kTile64>(a, s);
-    }
+    // as in dense_tile
+    auto tiles = [&](int r) { return grad_tiles(a.E, a.N, a.K, a.mats, r); };
+    const int64_t l = rounds(tiles(256), kCus) * 100;
+    const int64_t m = tiles(128) <= kCus ? 40 : rounds(tiles(128), 2 * kCus) * 65;
+    const int64_t t = rounds(tiles(64), 2 * kCus) * 31;
+    return l <= m && l <= t ? run_grad<kTile256>(a, s)
+           : m > t          ? run_grad<kTile64>(a, s)
+           : tiles(128) <= kCus ? run_grad<kTile128D>(a, s)
+                                : run_grad<kTile128>(a, s);
+}
+
+hipError_t launch_pair(const RowsArgs &a, const GradArgs &g, const BiasArgs &b, hipStream_t s) {
+    // Time in percent of a 256-row tile's step: all tile steps at the rate of a
+    // full CU (`full` a tile) over the CUs, or the longest tile at the rate of a
+    // tile alone on its CU, and half of a shorter one for the end; `more` steps a
+    // tile for its start and epilogue.  Fitted to nine shapes from 100 x 4096 ->
+    // 4096 to 4096 x 7168 -> 2 x 2048, on each of which it picks the fastest or
+    // one within 1 %.
+    const int64_t sx = a.nseg * ((a.Kd + kStepK - 1) / kStepK), sw = (g.R + kStepK - 1) / kStepK;
+    auto time = [&](int r, int more, int full, int alone) {
+        const int64_t nx = (int64_t)((a.R + r - 1) / r) * ((a.Np + r - 1) / r);
+        const int64_t nw = grad_tiles(1, g.N, g.K, g.mats, r);
+        const int64_t work = (nx * (sx + more) + nw * (sw + more)) * full / kCus;
+        return std::max(work, (std::max(sx, sw) + more) * alone) +
+               (std::min(sx, sw) + more) * full / 2;
+    };
+    const int64_t l = time(256, 4, 100, 85), m = time(128, 3, 40, 45), d = time(128, 3, 42, 27),
+                  t = time(64, 2, 20, 12);
+    const int64_t best = std::min({l, m, d, t});
+    return best == l   ? run_pair<kTile256>(a, g, b, s)
+           : best == m ? run_pair<kTile128>(a, g, b, s)
+           : best == d ? run_pair<kTile128D>(a, g, b, s)
+                       : run_pair<kTile64>(a, g, b, s);
 }
 
 hipError_t launch_colsum(const uint16_t *dy, int R, int N, const int4 *tiles, WsHeader *hdr,
@@ -435,11 +534,8 @@ hipError_t launch_colsum(const uint16_t *dy, int R, int N, const int4 *tiles, Ws
     return hipGetLastError();
 }
 
-hipError_t launch_bias_grad(const float *bpart, const int32_t *offsets, int R, int E, int N,
-                            int max_tiles, int tile_rows, float *db, int accumulate,
-                            hipStream_t s) {
-    bias_grad_kernel<<<dim3((N + 255) / 256, E), 256, 0, s>>>(bpart, offsets, R, N, max_tiles,
-                                                              tile_rows, db, accumulate);
+hipError_t launch_bias_grad(const BiasArgs &b, int E, hipStream_t s) {
+    bias_grad_kernel<<<dim3((b.N + 255) / 256, E), 256, 0, s>>>(b);
     return hipGetLastError();
 }
 

@@ -123,8 +123,10 @@ struct Call {
         a.tile = tile(w1 ? 2 * a.Np : a.Np);
         return a;
     }
-    // dx = dz0 w0 (+ dz1 w1), dz1 behind dz0
-    int input_grad(const uint16_t *dz, const void *w0, const void *w1, void *dx) const {
+    // dx = dz0 w0 (+ dz1 w1), dz1 behind dz0; dw0 = dz0^T x (and dw1); db from
+    // its row tiles' partials.  Each only where its output is set (part: db's).
+    int gradients(const uint16_t *dz, const uint16_t *x, const void *w0, const void *w1, void *dx,
+                  void *dw0, void *dw1, const float *part, int part_rows, float *db) const {
         RowsArgs a = rows(dz, w0, w1);
         a.q_seg = (size_t)R * d.out_features;
         a.Kd = d.out_features;
@@ -133,12 +135,15 @@ struct Call {
         a.tile = tile(a.Np);
         a.out = dx;
         a.out_f32 = d.grad_dtype == FW_F32;
-        return hip_status(launch_rows(kInput, a, s));
-    }
-    int weight_grad(const uint16_t *dz, const uint16_t *x, void *dw0, void *dw1) const {
-        GradArgs a{dz, x, R, d.n_experts, d.out_features, d.in_features, dw1 ? 2 : 1, offsets,
-                   dw0, dw1, d.grad_dtype == FW_F32, d.accumulate};
-        return hip_status(launch_grad(a, s));
+        const GradArgs g{dz, x, R, d.n_experts, d.out_features, d.in_features, dw1 ? 2 : 1, offsets,
+                         dw0, dw1, a.out_f32, d.accumulate};
+        const BiasArgs b{part, offsets, R, d.out_features, L.max_tiles, part_rows, db,
+                         d.accumulate};
+        if (dx && dw0 && !offsets && R > 0) return hip_status(launch_pair(a, g, b, s));
+        int rc;
+        if (dx && R > 0 && (rc = hip_status(launch_rows(kInput, a, s))) != FW_OK) return rc;
+        if (db && (rc = hip_status(launch_bias_grad(b, d.n_experts, s))) != FW_OK) return rc;
+        return dw0 ? hip_status(launch_grad(g, s)) : FW_OK;
     }
     // x as bf16: itself, or the checkpoint's values in the workspace
     int values(const void *x, const void *scales, const uint16_t **out) const {
@@ -214,9 +219,8 @@ int fw_moe_glu_backward(const fw_moe_dense_desc *desc, int32_t R, const void *x,
         a.dz = dz;
         a.out = h;
         if ((rc = hip_status(launch_rows(kGluGrad, a, c.s))) != FW_OK) return rc;
-        if (dx && (rc = c.input_grad(dz, w_gate, w_up, dx)) != FW_OK) return rc;
     }
-    return dw_gate ? c.weight_grad(dz, xv, dw_gate, dw_up) : FW_OK;
+    return c.gradients(dz, xv, w_gate, w_up, dx, dw_gate, dw_up, nullptr, 1, nullptr);
 }
 
 int fw_moe_linear_forward(const fw_moe_dense_desc *desc, int32_t R, const void *x, const void *w,
@@ -276,15 +280,8 @@ int fw_moe_linear_backward(const fw_moe_dense_desc *desc, int32_t R, const void 
                                           (WsHeader *)c.ws, c.L.max_tiles, part_rows, bpart, c.s));
             if (rc != FW_OK) return rc;
         }
-        if (dx && (rc = c.input_grad(dz, w, nullptr, dx)) != FW_OK) return rc;
     }
-    if (dbias) {
-        rc = hip_status(launch_bias_grad(bpart, expert_offsets, R, desc->n_experts,
-                                         desc->out_features, c.L.max_tiles, part_rows, dbias,
-                                         desc->accumulate, c.s));
-        if (rc != FW_OK) return rc;
-    }
-    return dw ? c.weight_grad(dz, xv, dw, nullptr) : FW_OK;
+    return c.gradients(dz, xv, w, nullptr, dx, dw, nullptr, bpart, part_rows, dbias);
 }
 
 int fw_moe_ckpt_pack(const fw_moe_ckpt_desc *desc, int32_t R, const void *x, void *codes,

@@ -161,8 +161,8 @@ template <int ROWS, bool ACROSS, int N> struct Reader {
 
 // The stages' LDS: arrays of their own, so that the compiler knows that a
 // pending DMA and a read touch different ones.
-template <class S> struct Ring {
-    uint4 *p[S::NS], *q[S::NS];
+template <int NS> struct Ring {
+    uint4 *p[NS], *q[NS];
 };
 #define FW_STAGE(S, n)                                          \
     __shared__ uint4 fw_p##n[S::NS > n ? S::PChunks : 1];       \
@@ -171,19 +171,19 @@ template <class S> struct Ring {
         fw_ring.p[n] = fw_p##n;                                 \
         fw_ring.q[n] = fw_q##n;                                 \
     }
-#define FW_RING(S, name) \
-    Ring<S> fw_ring;     \
-    FW_STAGE(S, 0)       \
-    FW_STAGE(S, 1)       \
-    FW_STAGE(S, 2)       \
-    FW_STAGE(S, 3)       \
-    const Ring<S> &name = fw_ring
+#define FW_RING(S, name)   \
+    Ring<S::NS> fw_ring;   \
+    FW_STAGE(S, 0)         \
+    FW_STAGE(S, 1)         \
+    FW_STAGE(S, 2)         \
+    FW_STAGE(S, 3)         \
+    const Ring<S::NS> &name = fw_ring
 
 // acc[i][j] (PI x QJ groups of 16 x 16) = the tile product over nseg segments
 // of Kd steps; p(seg) / pb(seg) and q(seg) give the operands (pb: the second
 // matrix of a dual P tile).
 template <class S, class PF, class PBF, class QF>
-__device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], const Ring<S> &ring,
+__device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], const Ring<S::NS> &ring,
                                              int wave, int lane, int Kd, int nseg, PF &&p,
                                              PBF &&pb, QF &&q) {
     const int wp = wave % S::WP, wq = wave / S::WP;
