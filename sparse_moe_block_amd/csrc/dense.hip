@@ -51,6 +51,20 @@ __device__ __forceinline__ void store8(void *out, int f32, size_t at, const floa
     }
 }
 
+// store8 past the caches, for outputs larger than they are.
+__device__ __forceinline__ void stream8(void *out, int f32, size_t at, const float *v) {
+    typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+    if (f32) {
+        f4 *p = (f4 *)((float *)out + at);
+        __builtin_nontemporal_store(f4{v[0], v[1], v[2], v[3]}, p);
+        __builtin_nontemporal_store(f4{v[4], v[5], v[6], v[7]}, p + 1);
+    } else {
+        __builtin_nontemporal_store(u4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                       pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])},
+                                    (u4 *)((uint16_t *)out + at));
+    }
+}
+
 __global__ __launch_bounds__(kPrepThreads) void dense_schedule_kernel(
     const int32_t *__restrict__ offsets, int E, int R, int tile_rows, int max_tiles,
     int4 *__restrict__ active, int4 *__restrict__ tiles, int *__restrict__ split_cnt,
@@ -285,7 +299,8 @@ __device__ __forceinline__ void grad_tile(const GradArgs &a, const Ring<S::NS> &
 #pragma unroll
             for (int t = 0; t < 8; ++t) v[t] += o[t];
         }
-        store8(dw, a.out_f32, place(n, k), v);
+        if (a.stream) stream8(dw, a.out_f32, place(n, k), v);
+        else store8(dw, a.out_f32, place(n, k), v);
     });
 }
 

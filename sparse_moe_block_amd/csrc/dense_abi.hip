@@ -135,8 +135,11 @@ struct Call {
         a.tile = tile(a.Np);
         a.out = dx;
         a.out_f32 = d.grad_dtype == FW_F32;
-        const GradArgs g{dz, x, R, d.n_experts, d.out_features, d.in_features, dw1 ? 2 : 1, offsets,
-                         dw0, dw1, a.out_f32, d.accumulate};
+        const int mats = dw1 ? 2 : 1;
+        const size_t bytes = (size_t)mats * d.n_experts * d.out_features * d.in_features *
+                             (a.out_f32 ? 4 : 2);
+        const GradArgs g{dz, x, R, d.n_experts, d.out_features, d.in_features, mats, offsets, dw0,
+                         dw1, a.out_f32, d.accumulate, bytes > ((size_t)256 << 20)};
         const BiasArgs b{part, offsets, R, d.out_features, L.max_tiles, part_rows, db,
                          d.accumulate};
         if (dx && dw0 && !offsets && R > 0) return hip_status(launch_pair(a, g, b, s));
