@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kPrepThreads) void dense_schedule_kernel(
 // the tile list, which walks blocks of kBlockRows row tiles column by column,
 // so that an XCD's workgroups in flight share few weight and few row panels in
 // its L2.  -1: none.
-constexpr int kBlockRows = 8;
+constexpr int kBlockRows = 4;   // 8: up to 3 % slower
 __device__ __forceinline__ int dense_block(int block_id, int row_tiles, int col_tiles, int &ct) {
     const int total = row_tiles * col_tiles, per = (total + 7) / 8;
     const int idx = block_id / 8, id = (block_id % 8) * per + idx;
