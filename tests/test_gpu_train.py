@@ -380,7 +380,8 @@ CHOICES = [(16, 512, 264, 1), (17, 512, 264, 1), (32, 4096, 72, 1), (33, 4096, 7
            (64, 264, 136, 8), (65, 264, 136, 8), (512, 264, 136, 8), (511, 264, 136, 8),
            (2048, 264, 136, 8), (2050, 264, 520, 8), (2047, 72, 520, 8), (300, 264, 4104, 1),
            (1500, 264, 4104, 1), (4100, 72, 4104, 1), (2100, 1032, 8200, 1), (5000, 520, 520, 1),
-           (100, 1032, 1032, 64), (40, 2056, 4104, 16)]
+           (100, 1032, 1032, 64), (40, 2056, 4104, 16), (777, 1536, 4096, 1), (1100, 2048, 264, 1),
+           (1300, 264, 4104, 1)]
 
 
 @pytest.mark.parametrize("R,K,N,E", CHOICES)
@@ -413,4 +414,13 @@ def test_tile_choices(R, K, N, E):
         for name, got, want, bound in checks:
             if got.numel():
                 ref.check(f"{name} expert {e}", got, want.cpu(), bound.cpu())
+    # dx and dw by launches of their own, in the tile shapes that those take: the
+    # sums run over the reduction in the same order, so the same bits
+    dx2, dwg2, dwu2, lx2, lw2 = (torch.full_like(t, 9.0) for t in (dx, dwg, dwu, lx, lw))
+    fw.fw_moe_glu_backward(d, R, x, None, wg, wu, c.offsets, dy, dx2, None, None, None, ws)
+    fw.fw_moe_glu_backward(d, R, x, None, wg, wu, c.offsets, dy, None, dwg2, dwu2, None, ws)
+    fw.fw_moe_linear_backward(d, R, x, None, wg, b, c.offsets, dy, lx2, None, None, ws)
+    fw.fw_moe_linear_backward(d, R, x, None, wg, b, c.offsets, dy, None, lw2, None, ws)
+    for p, q in ((dx, dx2), (dwg, dwg2), (dwu, dwu2), (lx, lx2), (lw, lw2)):
+        assert torch.equal(p, q)
     assert fw.fw_moe_read_status(ws) == 0
