@@ -53,6 +53,27 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(RowsArgs a,
             x[q] = a.q + (size_t)min(rb + 16 * q + p, n - 1) * K + k8;
             acc[q] = f4{0.f, 0.f, 0.f, 0.f};
         }
+        // what the thread's outputs need besides the sums, on its way meanwhile.
+        // Lane l of group q: row rb + 16 q + l % 16, weight rows 4 (l / 16) .. + 3;
+        // gated: lanes below 32 hold the gate rows, those above the up rows
+        constexpr int T = GLU ? 32 : 64;
+        const int oq = threadIdx.x / T, ol = threadIdx.x % T;
+        const int row = rb + 16 * oq + (ol & 15), col = f0 + 4 * (ol >> 4);
+        const bool mine = (int)threadIdx.x < T * NQ && row < n && col < a.Np;
+        const size_t at = (size_t)row * a.Np + col;
+        float4 bias{0.f, 0.f, 0.f, 0.f};
+        uint4 res{0, 0, 0, 0};
+        if constexpr (!GLU) {
+            if (mine && a.bias) bias = *(const float4 *)(a.bias + (size_t)e * a.Np + col);
+            if (mine && a.residual) {
+                if (a.out_f32) {
+                    res = *(const uint4 *)((const float *)a.residual + at);
+                } else {
+                    const uint2 r = *(const uint2 *)((const uint16_t *)a.residual + at);
+                    res = uint4{r.x << 16, r.x & 0xFFFF0000u, r.y << 16, r.y & 0xFFFF0000u};
+                }
+            }
+        }
         for (int s = s0; s < s1; s += U) {
             uint4 wv[U], xv[U][NQ];
 #pragma unroll
@@ -86,43 +107,32 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(RowsArgs a,
 #pragma unroll
         for (int q = 0; q < NQ; ++q) part[wave][q][lane] = acc[q];
         __syncthreads();
-        // lane l of group q: row rb + 16 q + l % 16, weight rows 4 (l / 16) .. + 3;
-        // gated: lanes below 32 hold the gate rows, those above the up rows
-        constexpr int T = GLU ? 32 : 64;
-        if ((int)threadIdx.x < T * NQ) {
-            const int q = threadIdx.x / T, l = threadIdx.x % T;
-            const int row = rb + 16 * q + (l & 15), col = f0 + 4 * (l >> 4);
-            f4 z = part[0][q][l], u{};
+        if (mine) {
+            f4 z = part[0][oq][ol], u{};
 #pragma unroll
-            for (int i = 1; i < kFewWaves; ++i) z += part[i][q][l];
+            for (int i = 1; i < kFewWaves; ++i) z += part[i][oq][ol];
             if constexpr (GLU) {
-                u = part[0][q][l + 32];
+                u = part[0][oq][ol + 32];
 #pragma unroll
-                for (int i = 1; i < kFewWaves; ++i) u += part[i][q][l + 32];
+                for (int i = 1; i < kFewWaves; ++i) u += part[i][oq][ol + 32];
             }
-            if (row < n && col < a.Np) {
-                const size_t at = (size_t)row * a.Np + col;
-                float v[4];
+            const float b4[4] = {bias.x, bias.y, bias.z, bias.w};
+            const uint32_t r4[4] = {res.x, res.y, res.z, res.w};
+            float v[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if constexpr (GLU) {
-                        v[t] = act_value(a.fn, z[t]) * u[t];
-                    } else {
-                        const float bias = a.bias ? a.bias[(size_t)e * a.Np + col + t] : 0.f;
-                        v[t] = act_value(a.fn, z[t] + bias);
-                        if (a.residual)
-                            v[t] += a.out_f32 ? ((const float *)a.residual)[at + t]
-                                              : __uint_as_float(
-                                                    (uint32_t)((const uint16_t *)a.residual)[at + t]
-                                                    << 16);
-                    }
+            for (int t = 0; t < 4; ++t) {
+                if constexpr (GLU) {
+                    v[t] = act_value(a.fn, z[t]) * u[t];
+                } else {
+                    v[t] = act_value(a.fn, z[t] + b4[t]);
+                    if (a.residual) v[t] += __uint_as_float(r4[t]);
                 }
-                if (a.out_f32)
-                    *(float4 *)((float *)a.out + at) = float4{v[0], v[1], v[2], v[3]};
-                else
-                    *(uint2 *)((uint16_t *)a.out + at) =
-                        uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
             }
+            if (a.out_f32)
+                *(float4 *)((float *)a.out + at) = float4{v[0], v[1], v[2], v[3]};
+            else
+                *(uint2 *)((uint16_t *)a.out + at) =
+                    uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
         }
         __syncthreads();
     }
