@@ -2,27 +2,28 @@
 // the weights' bytes, each of which is read once per 16 NQ rows of its expert.
 //
 // A workgroup takes 16 weight rows of one expert (gated: 8 gate rows and the 8
-// up rows of the same features) and all of the reduction, a quarter of it per
+// up rows of the same features) and all of the reduction, an eighth of it per
 // wavefront.  The weights are the MFMA's first operand, loaded straight from
 // memory in its layout (lane l: row l % 16, steps 8 (l / 16) .. + 7, 16 bytes),
-// eight (four) loads in flight per wavefront; NQ groups of 16 rows of x are the
-// second.  The four partial tiles meet in LDS and are summed in order.
+// four loads in flight per wavefront; NQ groups of 16 rows of x are the second.
+// The eight partial tiles meet in LDS and are summed in order.
 //
 // Measured (graph replays): 128 rows over 128 experts, 2048 -> 2 x 768, 511 MB of
-// weights: 85 us (6.0 TB/s) with four wavefronts a workgroup, 121 us with eight,
-// 102 us as 64-row tiles through LDS; one row, 7168 -> 2 x 2048, 59 MB: 12.5 us,
-// 33 us as 64-row tiles, which meet at a rendezvous every 128 steps.
+// weights: 81.5 us (6.3 TB/s); 102 us as 64-row tiles through LDS, 120 us with
+// eight loads in flight (half the workgroups a CU).  One row, 7168 -> 2 x 2048, 59
+// MB: 11.2 us (5.2 TB/s); 13.7 us with four wavefronts of eight loads, 33 us as
+// 64-row tiles.
 #include "dense_core.h"
 
 namespace fw {
 namespace {
 
-constexpr int kFewWaves = 4;
+constexpr int kFewWaves = 8;
 
 template <bool GLU, int NQ>
 __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(RowsArgs a,
                                                              const int32_t *__restrict__ offsets) {
-    constexpr int U = NQ == 1 ? 8 : 4;   // steps in flight
+    constexpr int U = 4;   // steps in flight
     __shared__ f4 part[kFewWaves][NQ][64];
     const int e = blockIdx.y, lane = threadIdx.x % kWave, wave = wave_id();
     int b = 0, n = a.R;
