@@ -7,14 +7,19 @@
 // rows, "along") or across it (its rows are reduction steps, "across": weight
 // rows in dx, activation and gradient rows in dW).  Along: LDS holds [rows][64]
 // in 16-byte chunks, chunk c of row r at c ^ (r / 2 % 8), and a lane's MFMA
-// operand (row l % 32, steps 8 (l / 32) .. + 7 of a 16-step slice) is one
+// operand (row l % 16, steps 8 (l / 16) .. + 7 of a 32-step slice) is one
 // ds_read_b128: the sixteen lanes served at once read sixteen rows, two rows to
 // a 256-byte turn of the banks, at sixteen different places in it (with
-// c ^ (r % 8) rows eight apart met: half of the LDS cycles were conflicts).  Across: LDS
-// holds [64][cols] with the 64-byte column blocks of row k moved by xor k % 4,
-// and the operand is two ds_read_b64_tr_b16, each 16-lane group reading four
-// rows x 32 bytes and receiving them transposed (four steps of one column per
-// lane); the xor puts the four rows' blocks into different banks.
+// c ^ (r % 8) rows eight apart met: half of the LDS cycles were conflicts).
+// Across: LDS holds [64][cols] with the 32-byte column blocks of a row moved by
+// xor (across_key), and the operand is two ds_read_b64_tr_b16, each 16-lane
+// group reading four rows x 32 bytes and receiving them transposed (four steps
+// of one column per lane); the xor puts the eight rows that 32 lanes read at
+// once into different banks.
+//
+// v_mfma_f32_16x16x32_bf16 rather than the 32x32x16 form: the large tiles run at
+// the clock that power allows, and it moves half as many accumulator registers a
+// flop (4096 x 7168 -> 2 x 2048: 178 us against 190).
 //
 // The first MFMA operand is P and the accumulator holds, per lane, four
 // consecutive P indices of one Q index: P is the output's contiguous dimension.
