@@ -61,9 +61,9 @@ struct RowsArgs {
     float *bpart;              // kLinGrad: [row tile][Np] or nullptr
 };
 constexpr int kCus = 256;      // the MI355X's compute units
-// The tile shape: one choice per call when the row tiles come from a schedule,
-// per product (`cols` output columns) otherwise.
-DenseTile dense_tile(int R, int E, int cols, bool grouped);
+// The tile shape of a product with `cols` output columns; widest: the most columns
+// of the call's products where the row tiles come from a schedule, 0 otherwise.
+DenseTile dense_tile(int R, int E, int cols, int widest);
 hipError_t launch_rows(DenseOp op, const RowsArgs &a, hipStream_t s);
 
 // kGlu and kLinear for few rows an expert (dense_few.hip), straight from

@@ -1,7 +1,7 @@
 // The bf16 training products: the gated feed-forward products and the linear
 // product with their epilogues, their input gradients and their weight and
 // bias gradients, for one matrix or one per expert (rows grouped by
-// expert_offsets).  Every product runs on v_mfma_f32_32x32x16_bf16 with fp32
+// expert_offsets).  Every product runs on v_mfma_f32_16x16x32_bf16 with fp32
 // accumulators (dense_core.h).
 //
 // Backward.  g, u (and z) are formed again from x instead of being kept: their
@@ -476,14 +476,25 @@ int64_t rounds(int64_t tiles, int64_t per) { return (tiles + per - 1) / per; }
 // 4096 in 16.1 us with 224 tiles of 128, 22.7 us with 832 of 64.  Rows in groups
 // of about 128 (2048 -> 2 x 768, 128 groups): 254 us with wide tiles, 265 us with
 // 128 x 128.
-DenseTile dense_tile(int R, int E, int cols, bool grouped) {
-    if (grouped) return R >= E * 256LL ? kTile256 : R >= E * 64LL ? kTileWide : kTile64;
-    auto tiles = [&](int r, int c) { return (int64_t)((R + r - 1) / r) * ((cols + c - 1) / c); };
-    const int64_t l = rounds(tiles(256, 256), kCus) * 100;
-    const int64_t m = tiles(128, 128) <= kCus ? 40 : rounds(tiles(128, 256), kCus) * 60;
-    const int64_t t = rounds(tiles(64, 64), 2 * kCus) * 31;
+//
+// Rows by expert take one row count a call, for the schedule: the best one for
+// `widest` columns if the experts have equal rows; the shape with that many rows
+// is the product's own choice.
+DenseTile dense_tile(int R, int E, int cols, int widest) {
+    auto tiles = [&](int r, int c, int n) {
+        const int64_t rt = widest ? (int64_t)E * (((R + E - 1) / E + r - 1) / r) : (R + r - 1) / r;
+        return rt * ((n + c - 1) / c);
+    };
+    auto mid = [&](int n) {
+        return tiles(128, 128, n) <= kCus ? 40 : rounds(tiles(128, 256, n), kCus) * 60;
+    };
+    const int n = widest ? widest : cols;
+    if (widest && R <= 64LL * E) return kTile64;   // 32 rows an expert: 165 us, 192 wide
+    // experts of unequal rows leave more of a smaller tile's last one empty
+    const int64_t l = rounds(tiles(256, 256, n), kCus) * (widest ? 87 : 100), m = mid(n);
+    const int64_t t = rounds(tiles(64, 64, n), 2 * kCus) * 31;
     return l <= m && l <= t ? kTile256
-           : m <= t         ? (tiles(128, 128) <= kCus ? kTile128D : kTileWide)
+           : m <= t         ? (tiles(128, 128, cols) <= kCus ? kTile128D : kTileWide)
                             : kTile64;
 }
 

@@ -97,11 +97,14 @@ struct Call {
 
     int schedule() const {
         return offsets ? hip_status(launch_dense_schedule(offsets, d.n_experts, R,
-                                                          tile_rows(tile(0)), L, ws, s))
+                                                          tile_rows(tile(8)), L, ws, s))
                        : FW_OK;
     }
     // the tile shape of a product with cols output columns (both matrices')
-    DenseTile tile(int cols) const { return dense_tile(R, d.n_experts, cols, offsets != nullptr); }
+    DenseTile tile(int cols) const {
+        return dense_tile(R, d.n_experts, cols,
+                          offsets ? std::max(d.in_features, d.out_features) : 0);
+    }
     bool few() const { return few_rows(R, d.n_experts, d.in_features); }
     const int4 *tiles() const { return offsets ? (const int4 *)(ws + L.tiles) : nullptr; }
     // forward-shaped product: x [R][K] times weights [N][K]
