@@ -381,7 +381,8 @@ CHOICES = [(16, 512, 264, 1), (17, 512, 264, 1), (32, 4096, 72, 1), (33, 4096, 7
            (2048, 264, 136, 8), (2050, 264, 520, 8), (2047, 72, 520, 8), (300, 264, 4104, 1),
            (1500, 264, 4104, 1), (4100, 72, 4104, 1), (2100, 1032, 8200, 1), (5000, 520, 520, 1),
            (100, 1032, 1032, 64), (40, 2056, 4104, 16), (777, 1536, 4096, 1), (1100, 2048, 264, 1),
-           (1300, 264, 4104, 1)]
+           (1300, 264, 4104, 1), (6000, 2048, 2056, 8), (2000, 2048, 2056, 12),
+           (1100, 2048, 1032, 4), (4100, 2056, 2048, 1), (2048, 4104, 4096, 1)]
 
 
 @pytest.mark.parametrize("R,K,N,E", CHOICES)
