@@ -362,9 +362,11 @@ __device__ __forceinline__ void tile_product(f4 (&acc)[S::PI][S::QJ], const Ring
 // row instead of the accumulators' 32.  The way there is LDS, 16 rows at a
 // time, private to the wavefront, the 16-byte columns of a row moved by an xor
 // of the row against bank conflicts.  lds: a buffer of the product, free again.
+// APART: v[4..7] lie kOutCols / 2 columns behind v[0..3], so that each half of
+// eight fp32 values is a run of whole cache lines over the lanes of a row.
 template <class S> constexpr int kOutCols = S::BP / S::WP / (S::DUAL ? 2 : 1);
 
-template <class S, class Fetch, class Emit>
+template <class S, bool APART = false, class Fetch, class Emit>
 __device__ __forceinline__ void hand_out(const f4 (&acc)[S::PI][S::QJ], void *lds, int wave,
                                          int lane, Fetch &&fetch, Emit &&emit) {
     constexpr int CW = kOutCols<S>, LR = CW / 8;   // lanes a row
@@ -381,7 +383,8 @@ __device__ __forceinline__ void hand_out(const f4 (&acc)[S::PI][S::QJ], void *ld
     auto cell = [&](int r, int c) {
         return r * (CW / 4) + (c ^ (CW == 64 ? r : CW == 32 ? r >> 1 : r >> 2));
     };
-    const int rr = lane / LR % RP, rc = 8 * (lane % LR);
+    const int rr = lane / LR % RP, rc = (APART ? 4 : 8) * (lane % LR);
+    const int rc2 = rc + (APART ? CW / 2 : 4);
     const bool idle = lane / LR >= RP;
     const int col = wp * CW + rc;
 #pragma unroll
@@ -402,7 +405,7 @@ __device__ __forceinline__ void hand_out(const f4 (&acc)[S::PI][S::QJ], void *ld
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                const int lo = cell(p * RP + rr, rc / 4), hi = cell(p * RP + rr, rc / 4 + 1);
+                const int lo = cell(p * RP + rr, rc / 4), hi = cell(p * RP + rr, rc2 / 4);
                 float v[8], u[8];
                 *(f4 *)v = mine[lo];
                 *(f4 *)(v + 4) = mine[hi];

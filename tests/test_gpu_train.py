@@ -425,3 +425,35 @@ def test_tile_choices(R, K, N, E):
     for p, q in ((dx, dx2), (dwg, dwg2), (dwu, dwu2), (lx, lx2), (lw, lw2)):
         assert torch.equal(p, q)
     assert fw.fw_moe_read_status(ws) == 0
+
+
+# The last tile of dw has columns in one half of a lane's values only (8 to 32 of
+# 64) or in both; each tile shape, and gradients stored past the caches.
+@pytest.mark.parametrize("R,K,N,E", [(5, 8, 8, 1), (70, 40, 72, 3), (130, 104, 136, 1),
+                                     (300, 232, 264, 2), (600, 1000, 1096, 1),
+                                     (900, 2024, 2088, 1), (1024, 4128, 4104, 1),
+                                     (200, 1064, 1032, 70), (100, 4104, 2088, 8)])
+def test_weight_gradient_types(R, K, N, E):
+    """fp32 weight gradients against the formula, the bf16 ones as their rounding,
+    and accumulation as the sum of both."""
+    g = torch.Generator().manual_seed(R + K + N)
+    cuts = sorted(torch.randint(0, R + 1, (E - 1,), generator=g).tolist())
+    c = Case((R, K, N, None if E == 1 else [0] + cuts + [R]), seed=43)
+    d32, d16 = c.desc(fn="none", grad_dtype="f32"), c.desc(fn="none", grad_dtype="bf16")
+    acc = c.desc(fn="none", grad_dtype="f32", accumulate=True)
+    ws = c.ws(d32)
+    x, w, dy = c.x.to(DEV), c.w[0].to(DEV), c.dy.to(DEV)
+    for dx in (None, out(R, K, dtype=F32)):   # by itself, and joint with dx
+        dx16 = None if dx is None else out(R, K)
+        dw, low = out(E, N, K, dtype=F32), out(E, N, K)
+        start = torch.randn(E, N, K, device=DEV)
+        total = start.clone()
+        for d, a, b in ((d32, dx, dw), (d16, dx16, low), (acc, dx, total)):
+            fw.fw_moe_linear_backward(d, R, x, None, w, None, c.offsets, dy, a, b, None, ws)
+        for e, a, z in c.segs():
+            want, bound = ref.linear_backward(x[a:z].double(), w[e].double(), None,
+                                              dy[a:z].double(), "none", F32)[1]
+            ref.check(f"dw expert {e}", dw[e], want.cpu(), bound.cpu())
+        assert torch.equal(dw.to(BF16), low)
+        assert torch.equal(total, start + dw)
+    assert fw.fw_moe_read_status(ws) == 0
