@@ -245,7 +245,7 @@ __global__ __launch_bounds__(kThreads<TILE>, kBlocksPerCu<TILE>) void rows_kerne
         rt = xcd_row_tile(a.hdr, col_tiles, row_tiles, 0, 0, ct);
         // dx takes the experts from the last to the first: the weights that the
         // recomputation before it read last are still in the memory-side cache
-        // (a whole backward call of 128 experts: 552 -> 530 us)
+        // (4096 rows over 128 experts, 2048 -> 2 x 768, whole call: 562 -> 534 us)
         if (OP == kInput && rt >= 0) {
             const int xcd = blockIdx.x % 8, n = min(ld_const(&a.hdr->n_tiles), row_tiles);
             rt = ld_const(&a.hdr->xcd_first[xcd]) +
